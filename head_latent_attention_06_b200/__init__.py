@@ -19,12 +19,13 @@ LIB_PATH = os.path.join(PKG, "libmla_b200.so")
 D_C, D_R, D_N, D_V, PAGE = 512, 64, 128, 128, 64
 MAX_SPLITS = 128
 KV_BF16, KV_FP8_E4M3, KV_Q8_0, KV_Q4_0 = 0, 1, 2, 3
+PROB_FP32, PROB_BF16 = 0, 1
 Q8_BLOCKS = (D_C + D_R) // 32   # q8_0: scale blocks of a 576-value row
 
 STATUS = {
     0: "MLA_OK", 1: "MLA_ERR_INVALID_VALUE", 2: "MLA_ERR_UNSUPPORTED", 3: "MLA_ERR_MISALIGNED",
     4: "MLA_ERR_WORKSPACE_TOO_SMALL", 5: "MLA_ERR_CUDA", 6: "MLA_ERR_DEVICE_TIMEOUT",
-    7: "MLA_ERR_BAD_BLOCK_TABLE", 8: "MLA_ERR_BAD_SEQ_LEN",
+    7: "MLA_ERR_BAD_BLOCK_TABLE", 8: "MLA_ERR_BAD_SEQ_LEN", 9: "MLA_ERR_BAD_TOKEN",
 }
 
 # Every symbol include/mla.h declares.
@@ -33,7 +34,9 @@ EXPORTS = ("mla_absorb_q", "mla_decode_workspace_size", "mla_decode_num_splits",
            "mla_status_string", "mla_decode_paged_noalloc", "mla_noalloc_init",
            "mla_get_status_noalloc", "mla_write_kv_workspace_size", "mla_write_kv",
            "mla_set_decode_kernel", "mla_set_device_wait_limit", "mla_fold_hadamard", "mla_prefill_workspace_size",
-           "mla_prefill", "mla_decode_step_workspace_size", "mla_decode_step_launches", "mla_decode_step")
+           "mla_prefill", "mla_decode_step_workspace_size", "mla_decode_step_launches", "mla_decode_step",
+           "mla_append_workspace_size", "mla_append_kv", "mla_prefill_packed_workspace_size",
+           "mla_prefill_packed", "mla_verify_workspace_size", "mla_verify_draft")
 
 DECODE_AUTO, DECODE_WARP_MMA = 0, 1
 
@@ -109,6 +112,55 @@ class StepArgs(ctypes.Structure):
     ]
 
 
+class AppendArgs(ctypes.Structure):
+    """Mirror of ``mla_append_args_t`` (field order and types must match)."""
+    _fields_ = [
+        ("c", ctypes.c_void_p), ("k_pe", ctypes.c_void_p), ("q_pe", ctypes.c_void_p),
+        ("k_pe_out", ctypes.c_void_p), ("q_pe_out", ctypes.c_void_p),
+        ("kv_cache", ctypes.c_void_p), ("kv_scale", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("c_tok", ctypes.c_int64), ("k_pe_tok", ctypes.c_int64),
+        ("q_pe_tok", ctypes.c_int64), ("q_pe_head", ctypes.c_int64),
+        ("k_pe_out_tok", ctypes.c_int64), ("q_pe_out_tok", ctypes.c_int64), ("q_pe_out_head", ctypes.c_int64),
+        ("n_tok", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32),
+        ("d_c", ctypes.c_int32), ("d_r", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("max_pages_per_seq", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32), ("rope_base", ctypes.c_float),
+    ]
+
+
+class PrefillPackedArgs(ctypes.Structure):
+    """Mirror of ``mla_prefill_packed_args_t`` (field order and types must match)."""
+    _fields_ = [
+        ("q_nope", ctypes.c_void_p), ("q_pe", ctypes.c_void_p),
+        ("k_nope", ctypes.c_void_p), ("k_pe", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("cu_seqlens", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("q_nope_tok", ctypes.c_int64), ("q_nope_head", ctypes.c_int64),
+        ("q_pe_tok", ctypes.c_int64), ("q_pe_head", ctypes.c_int64),
+        ("k_nope_tok", ctypes.c_int64), ("k_nope_head", ctypes.c_int64), ("k_pe_tok", ctypes.c_int64),
+        ("v_tok", ctypes.c_int64), ("v_head", ctypes.c_int64),
+        ("n_tok", ctypes.c_int32), ("B", ctypes.c_int32), ("H", ctypes.c_int32), ("H_kv", ctypes.c_int32),
+        ("d_n", ctypes.c_int32), ("d_r", ctypes.c_int32), ("d_v", ctypes.c_int32),
+        ("causal", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+    ]
+
+
+class VerifyArgs(ctypes.Structure):
+    """Mirror of ``mla_verify_args_t`` (field order and types must match)."""
+    _fields_ = [
+        ("target_probs", ctypes.c_void_p), ("draft_probs", ctypes.c_void_p),
+        ("draft_tokens", ctypes.c_void_p), ("num_draft", ctypes.c_void_p),
+        ("u_accept", ctypes.c_void_p), ("u_sample", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p), ("num_accepted", ctypes.c_void_p), ("new_lens", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("target_seq", ctypes.c_int64), ("target_row", ctypes.c_int64),
+        ("draft_seq", ctypes.c_int64), ("draft_row", ctypes.c_int64),
+        ("B", ctypes.c_int32), ("s_q", ctypes.c_int32), ("V", ctypes.c_int32), ("dtype", ctypes.c_int32),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -145,6 +197,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.mla_decode_step_launches.argtypes = [ps, ctypes.POINTER(ctypes.c_int32)]
     lib.mla_decode_step.argtypes = [ps, vp]
     lib.mla_fold_hadamard.argtypes = [vp, i32, vp, vp, i32, vp]
+    for name, kind in (("append", AppendArgs), ("prefill_packed", PrefillPackedArgs), ("verify", VerifyArgs)):
+        getattr(lib, f"mla_{name}_workspace_size").argtypes = [ctypes.POINTER(kind), ctypes.POINTER(ctypes.c_size_t)]
+    lib.mla_append_kv.argtypes = [ctypes.POINTER(AppendArgs), vp]
+    lib.mla_prefill_packed.argtypes = [ctypes.POINTER(PrefillPackedArgs), vp]
+    lib.mla_verify_draft.argtypes = [ctypes.POINTER(VerifyArgs), vp]
     lib.mla_status_string.argtypes = [ctypes.c_int]
     lib.mla_status_string.restype = ctypes.c_char_p
     for name in EXPORTS:
@@ -190,6 +247,64 @@ def _want(specs):
     for t, name, _, _, _ in specs:
         if t is not None and not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _want_one_device(specs):
+    """The last check of the packed and verification builders: every tensor on one
+    CUDA device, which the entry points then make current.  Returns that device."""
+    dev = None
+    for t, name, *_ in specs:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if dev is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, the others on {dev}")
+        dev = t.device
+    return dev
+
+
+def _want_views(specs):
+    """Like ``_want``, for tensors of which only the innermost dimension has to be
+    contiguous (strided views); the device is left to ``_want_one_device``."""
+    for t, name, dtypes, shape, optional in specs:
+        if t is None:
+            if optional:
+                continue
+            raise ValueError(f"{name} is required")
+        dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name}: its innermost dimension must be contiguous")
+
+
+def _want_dense(specs):
+    """``_want`` without the device check."""
+    _want_views([(t, n, d, t.shape if t is not None and s is None else s, o) for t, n, d, s, o in specs])
+    for t, name, *_ in specs:
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+
+
+def _call(fn, args, stream):
+    """Calls entry point ``fn`` on ``stream`` (default: torch's current stream of the
+    device that the arguments' tensors are on), with that device current."""
+    import torch
+    dev = getattr(args, "device", None)
+    if dev is None or dev.index == torch.cuda.current_device():
+        _check(fn, getattr(load(), fn)(ctypes.byref(args), _stream(stream)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, getattr(load(), fn)(ctypes.byref(args), _stream(stream)))
+
+
+def _workspace_size(fn, args) -> int:
+    n = ctypes.c_size_t(0)
+    _check(fn, getattr(load(), fn)(ctypes.byref(args), ctypes.byref(n)))
+    return int(n.value)
 
 
 def _tokens(t, name, H, d):
@@ -515,6 +630,160 @@ def mla_prefill(args: PrefillArgs, stream=None):
     _check("mla_prefill", load().mla_prefill(ctypes.byref(args), _stream(stream)))
 
 
+def make_append_args(*, c, k_pe, q_pe=None, k_pe_out=None, q_pe_out=None, kv_cache, kv_scale, block_table,
+                     cu_seqlens, seq_lens, workspace=None, rope_base=10000.0) -> AppendArgs:
+    """Fill an ``AppendArgs`` (packed tokens into the paged cache, rotation on the
+    way) from device tensors.  Shapes: c [n_tok][512], k_pe and k_pe_out [n_tok][64],
+    q_pe and q_pe_out [n_tok][H][64], all bf16 and strided views at will (the outputs
+    may be the inputs); the cache, scales and block table as for
+    ``make_write_kv_args``; cu_seqlens [B + 1] and seq_lens [B] int32."""
+    import torch
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    if c.dim() != 2 or kv_cache.dim() != 3 or block_table.dim() != 2 or (q_pe is not None and q_pe.dim() != 3):
+        raise ValueError("c must be [n_tok][512], q_pe [n_tok][H][64], kv_cache [pages][64][row], block_table [B][pages]")
+    if q_pe is None and q_pe_out is not None:
+        raise ValueError("q_pe_out without q_pe")
+    n, B, P = c.shape[0], block_table.shape[0], kv_cache.shape[0]
+    H = 0 if q_pe is None else q_pe.shape[1]
+    kind, sc_dtype, sc_tail, width = _cache_kind(kv_cache)
+    views = [(c, "c", bf16, (n, D_C), False), (k_pe, "k_pe", bf16, (n, D_R), False),
+             (q_pe, "q_pe", bf16, (n, H, D_R), True), (k_pe_out, "k_pe_out", bf16, (n, D_R), True),
+             (q_pe_out, "q_pe_out", bf16, (n, H, D_R), q_pe is None)]
+    dense = [(kv_cache, "kv_cache", (bf16, torch.float8_e4m3fn, torch.int8, torch.uint8), (P, PAGE, width), False),
+             (kv_scale, "kv_scale", sc_dtype or f32, (P, PAGE) + sc_tail, kind == KV_BF16),
+             (block_table, "block_table", i32, (B, block_table.shape[1]), False),
+             (cu_seqlens, "cu_seqlens", i32, (B + 1,), False), (seq_lens, "seq_lens", i32, (B,), False),
+             (workspace, "workspace", torch.uint8, None, True)]
+    _want_views(views)
+    _want_dense(dense)
+    a = AppendArgs()
+    a.device = _want_one_device(views + dense)
+    a.c, a.k_pe, a.q_pe, a.k_pe_out, a.q_pe_out = (_ptr(t) for t in (c, k_pe, q_pe, k_pe_out, q_pe_out))
+    a.c_tok, a.k_pe_tok = c.stride(0), k_pe.stride(0)
+    if k_pe_out is not None:
+        a.k_pe_out_tok = k_pe_out.stride(0)
+    if q_pe is not None:
+        a.q_pe_tok, a.q_pe_head = q_pe.stride(0), q_pe.stride(1)
+        a.q_pe_out_tok, a.q_pe_out_head = q_pe_out.stride(0), q_pe_out.stride(1)
+    a.kv_cache, a.kv_scale, a.block_table = _ptr(kv_cache), _ptr(kv_scale), _ptr(block_table)
+    a.cu_seqlens, a.seq_lens = _ptr(cu_seqlens), _ptr(seq_lens)
+    a.n_tok, a.B, a.H = n, B, H
+    a.d_c, a.d_r, a.page_size = D_C, D_R, PAGE
+    a.num_pages, a.max_pages_per_seq = P, block_table.shape[1]
+    a.kv_dtype = kind
+    a.rope_base = float(rope_base)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+    return a
+
+
+def mla_append_workspace_size(args: AppendArgs) -> int:
+    return _workspace_size("mla_append_workspace_size", args)
+
+
+def mla_append_kv(args: AppendArgs, stream=None):
+    """Appends packed tokens' latents and rotated RoPE keys to the paged cache and
+    rotates their queries' RoPE parts."""
+    _call("mla_append_kv", args, stream)
+
+
+def make_prefill_packed_args(*, q_nope, q_pe, k_nope, k_pe, v, cu_seqlens, out, lse, workspace=None,
+                             causal=True, softmax_scale) -> PrefillPackedArgs:
+    """Fill a ``PrefillPackedArgs`` (attention over packed prompts) from device
+    tensors.  Shapes: q_nope [n_tok][H][128], q_pe [n_tok][H][64] or None, k_nope and
+    v [n_tok][H_kv][128], k_pe [n_tok][64] or None with q_pe, all bf16 and strided
+    views at will; cu_seqlens [B + 1] int32; out [n_tok][H][128] bf16 and lse
+    [n_tok][H] fp32 or None, dense."""
+    import torch
+    bf16, f32, i32 = torch.bfloat16, torch.float32, torch.int32
+    if q_nope.dim() != 3 or k_nope.dim() != 3 or cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
+        raise ValueError("q_nope must be [n_tok][H][128], k_nope [n_tok][H_kv][128], cu_seqlens [B + 1]")
+    n, H, _ = q_nope.shape
+    H_kv = k_nope.shape[1]
+    if (q_pe is None) != (k_pe is None):
+        raise ValueError("q_pe and k_pe come together")
+    views = [(q_nope, "q_nope", bf16, (n, H, D_N), False), (q_pe, "q_pe", bf16, (n, H, D_R), True),
+             (k_nope, "k_nope", bf16, (n, H_kv, D_N), False), (k_pe, "k_pe", bf16, (n, D_R), True),
+             (v, "v", bf16, (n, H_kv, D_V), False)]
+    dense = [(cu_seqlens, "cu_seqlens", i32, None, False), (out, "out", bf16, (n, H, D_V), False),
+             (lse, "lse", f32, (n, H), True), (workspace, "workspace", torch.uint8, None, True)]
+    _want_views(views)
+    _want_dense(dense)
+    a = PrefillPackedArgs()
+    a.device = _want_one_device(views + dense)
+    a.q_nope, a.q_pe, a.k_nope, a.k_pe, a.v = (_ptr(t) for t in (q_nope, q_pe, k_nope, k_pe, v))
+    a.cu_seqlens, a.out, a.lse = _ptr(cu_seqlens), _ptr(out), _ptr(lse)
+    a.q_nope_tok, a.q_nope_head = q_nope.stride(0), q_nope.stride(1)
+    a.k_nope_tok, a.k_nope_head = k_nope.stride(0), k_nope.stride(1)
+    a.v_tok, a.v_head = v.stride(0), v.stride(1)
+    if q_pe is not None:
+        a.q_pe_tok, a.q_pe_head, a.k_pe_tok = q_pe.stride(0), q_pe.stride(1), k_pe.stride(0)
+    a.n_tok, a.B, a.H, a.H_kv = n, cu_seqlens.shape[0] - 1, H, H_kv
+    a.d_n, a.d_r, a.d_v = D_N, 0 if q_pe is None else D_R, D_V
+    a.causal = int(bool(causal))
+    a.softmax_scale = float(softmax_scale)
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+    return a
+
+
+def mla_prefill_packed_workspace_size(args: PrefillPackedArgs) -> int:
+    return _workspace_size("mla_prefill_packed_workspace_size", args)
+
+
+def mla_prefill_packed(args: PrefillPackedArgs, stream=None):
+    """Attention over packed prompts in the explicit form."""
+    _call("mla_prefill_packed", args, stream)
+
+
+def make_verify_args(*, target_probs, draft_probs, draft_tokens, u_accept, u_sample, tokens, num_accepted,
+                     num_draft=None, seq_lens=None, new_lens=None, workspace=None) -> VerifyArgs:
+    """Fill a ``VerifyArgs`` (verification of drafted tokens) from device tensors.
+    Shapes: target_probs [B][s_q][V] and draft_probs [B][s_q - 1][V] (or None: certain
+    drafts), both fp32 or both bf16, strided rows at will; draft_tokens int32 and
+    u_accept fp32 [B][s_q - 1]; num_draft [B] int32 or None; u_sample [B] fp32;
+    tokens [B][s_q], num_accepted, seq_lens and new_lens [B] int32."""
+    import torch
+    f32, i32 = torch.float32, torch.int32
+    if target_probs.dim() != 3:
+        raise ValueError("target_probs must be [B][s_q][V]")
+    B, s_q, V = target_probs.shape
+    if s_q < 1:
+        raise ValueError("target_probs must have at least one row per sequence")
+    views = [(target_probs, "target_probs", (f32, torch.bfloat16), (B, s_q, V), False),
+             (draft_probs, "draft_probs", target_probs.dtype, (B, s_q - 1, V), True)]
+    dense = [(draft_tokens, "draft_tokens", i32, (B, s_q - 1), False), (num_draft, "num_draft", i32, (B,), True),
+             (u_accept, "u_accept", f32, (B, s_q - 1), False), (u_sample, "u_sample", f32, (B,), False),
+             (seq_lens, "seq_lens", i32, (B,), new_lens is None), (tokens, "tokens", i32, (B, s_q), False),
+             (num_accepted, "num_accepted", i32, (B,), False), (new_lens, "new_lens", i32, (B,), True),
+             (workspace, "workspace", torch.uint8, None, True)]
+    _want_views(views)
+    _want_dense(dense)
+    a = VerifyArgs()
+    a.device = _want_one_device(views + dense)
+    a.target_probs, a.draft_probs, a.draft_tokens = _ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens)
+    a.num_draft, a.u_accept, a.u_sample = _ptr(num_draft), _ptr(u_accept), _ptr(u_sample)
+    a.seq_lens, a.tokens, a.num_accepted, a.new_lens = _ptr(seq_lens), _ptr(tokens), _ptr(num_accepted), _ptr(new_lens)
+    a.target_seq, a.target_row = target_probs.stride(0), target_probs.stride(1)
+    if draft_probs is not None:
+        a.draft_seq, a.draft_row = draft_probs.stride(0), draft_probs.stride(1)
+    a.B, a.s_q, a.V = B, s_q, V
+    a.dtype = PROB_FP32 if target_probs.dtype == f32 else PROB_BF16
+    if workspace is not None:
+        a.workspace, a.workspace_bytes = _ptr(workspace), workspace.numel()
+    return a
+
+
+def mla_verify_workspace_size(args: VerifyArgs) -> int:
+    return _workspace_size("mla_verify_workspace_size", args)
+
+
+def mla_verify_draft(args: VerifyArgs, stream=None):
+    """Accepts drafted tokens against the target's probabilities, draws the token
+    after them and shortens the cached lengths by the rejected ones."""
+    _call("mla_verify_draft", args, stream)
+
+
 def mla_get_status(workspace, stream=None) -> int:
     """Waits for the stream and returns (and clears) the device status word."""
     return int(load().mla_get_status(_ptr(workspace), _stream(stream)))
@@ -525,10 +794,15 @@ def mla_status_string(code: int) -> str:
 
 
 def alloc_workspace(args, device="cuda"):
-    """A zeroed workspace tensor sized for ``args`` (``DecodeArgs``,
-    ``WriteKvArgs`` or ``PrefillArgs``); also stored into ``args``."""
+    """A zeroed workspace tensor sized for ``args`` (any of the ``*Args``); also
+    stored into ``args``."""
     import torch
-    if isinstance(args, WriteKvArgs):
+    if isinstance(args, (AppendArgs, PrefillPackedArgs, VerifyArgs)):
+        n = {AppendArgs: mla_append_workspace_size, PrefillPackedArgs: mla_prefill_packed_workspace_size,
+             VerifyArgs: mla_verify_workspace_size}[type(args)](args)
+        if device == "cuda" and getattr(args, "device", None) is not None:
+            device = args.device
+    elif isinstance(args, WriteKvArgs):
         n = mla_write_kv_workspace_size(args)
     elif isinstance(args, StepArgs):
         n = mla_decode_step_workspace_size(args)

@@ -23,6 +23,9 @@ int write_kv_k_split(int n_tok, int d_h);
 cudaError_t launch_write_kv(const mla_write_kv_args_t*, cudaStream_t);
 size_t prefill_workspace_bytes(int B, int H, int Lmax);
 cudaError_t launch_prefill(const mla_prefill_args_t*, cudaStream_t);
+cudaError_t launch_append(const mla_append_args_t*, cudaStream_t);
+cudaError_t launch_prefill_packed(const mla_prefill_packed_args_t*, cudaStream_t);
+cudaError_t launch_verify(const mla_verify_args_t*, cudaStream_t);
 cudaError_t launch_fold_hadamard(void*, int, void*, void*, int, cudaStream_t);
 bool decode_step_fusable(const mla_decode_args_t*, int splits);
 size_t decode_step_flag_bytes();
@@ -142,6 +145,59 @@ mla_status_t check_prefill_shape(const mla_prefill_args_t* a) {
     return MLA_ERR_UNSUPPORTED;
   if (!(a->softmax_scale == a->softmax_scale)) return MLA_ERR_INVALID_VALUE;
   return MLA_OK;
+}
+
+// ---- packed batches and draft verification
+constexpr size_t kStatusBytes = 256;          // their workspace: the status word's header
+constexpr int32_t kMaxPacked = 1 << 30;       // rows, so that row indices of a tile stay below 2^31
+constexpr int32_t kMaxVocab = 1 << 20;
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A stride over `extent` rows or heads: positive multiples of 8 values, of no
+// meaning where there is only one.
+mla_status_t check_stride(int64_t s, int64_t extent) {
+  if (extent <= 1) return MLA_OK;
+  if (s <= 0) return MLA_ERR_INVALID_VALUE;
+  if (s >= (int64_t)1 << 38) return MLA_ERR_UNSUPPORTED;
+  return s % 8 ? MLA_ERR_MISALIGNED : MLA_OK;
+}
+
+mla_status_t check_append_shape(const mla_append_args_t* a) {
+  if (!a) return MLA_ERR_INVALID_VALUE;
+  if (a->B < 0 || a->H < 0 || a->n_tok < 0 || a->num_pages < 0 || a->max_pages_per_seq <= 0) return MLA_ERR_INVALID_VALUE;
+  if (a->n_tok > kMaxPacked || a->H > 128) return MLA_ERR_UNSUPPORTED;
+  if (a->d_c != kDc || a->d_r != kDr || a->page_size != kPage) return MLA_ERR_UNSUPPORTED;
+  if (a->max_pages_per_seq > 0x7fffffff / kPage) return MLA_ERR_UNSUPPORTED;
+  if (a->kv_dtype != MLA_KV_BF16 && a->kv_dtype != MLA_KV_FP8_E4M3 && a->kv_dtype != MLA_KV_Q8_0 &&
+      a->kv_dtype != MLA_KV_Q4_0)
+    return MLA_ERR_UNSUPPORTED;
+  if (!(a->rope_base > 0.f) || !isfinite(a->rope_base)) return MLA_ERR_INVALID_VALUE;
+  return MLA_OK;
+}
+
+mla_status_t check_packed_shape(const mla_prefill_packed_args_t* a) {
+  if (!a) return MLA_ERR_INVALID_VALUE;
+  if (a->B < 0 || a->H <= 0 || a->H_kv <= 0 || a->n_tok < 0) return MLA_ERR_INVALID_VALUE;
+  if (a->d_n != kDn || a->d_v != kDv || (a->d_r != kDr && a->d_r != 0)) return MLA_ERR_UNSUPPORTED;
+  if (a->H > 128 || a->n_tok > kMaxPacked) return MLA_ERR_UNSUPPORTED;
+  if (a->H % a->H_kv) return MLA_ERR_INVALID_VALUE;
+  if (!(a->softmax_scale > 0.f) || !isfinite(a->softmax_scale)) return MLA_ERR_INVALID_VALUE;
+  return MLA_OK;
+}
+
+mla_status_t check_verify_shape(const mla_verify_args_t* a) {
+  if (!a) return MLA_ERR_INVALID_VALUE;
+  if (a->B < 0 || a->s_q <= 0 || a->V <= 0) return MLA_ERR_INVALID_VALUE;
+  if (a->s_q > MLA_MAX_S_Q || a->V > kMaxVocab || a->B > (1 << 24)) return MLA_ERR_UNSUPPORTED;
+  if (a->dtype != MLA_PROB_FP32 && a->dtype != MLA_PROB_BF16) return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+mla_status_t check_status_workspace(void* ws, size_t bytes) {
+  if (!ws) return MLA_ERR_INVALID_VALUE;
+  if (!aligned16(ws)) return MLA_ERR_MISALIGNED;
+  return bytes < kStatusBytes ? MLA_ERR_WORKSPACE_TOO_SMALL : MLA_OK;
 }
 
 size_t write_kv_workspace(const mla_write_kv_args_t* a) {
@@ -400,6 +456,94 @@ mla_status_t mla_prefill(const mla_prefill_args_t* a, void* stream) {
   return from_cuda(launch_prefill(a, (cudaStream_t)stream));
 }
 
+mla_status_t mla_append_workspace_size(const mla_append_args_t* a, size_t* bytes) {
+  mla_status_t st = check_append_shape(a);
+  if (st != MLA_OK) return st;
+  if (!bytes) return MLA_ERR_INVALID_VALUE;
+  *bytes = kStatusBytes;
+  return MLA_OK;
+}
+
+mla_status_t mla_append_kv(const mla_append_args_t* a, void* stream) {
+  mla_status_t st = check_append_shape(a);
+  if (st == MLA_OK) st = check_status_workspace(a->workspace, a->workspace_bytes);
+  if (st != MLA_OK || a->B == 0 || a->n_tok == 0) return st;
+  if (!a->c || !a->k_pe || !a->kv_cache || !a->block_table || !a->cu_seqlens || !a->seq_lens) return MLA_ERR_INVALID_VALUE;
+  if ((a->H > 0 && (!a->q_pe || !a->q_pe_out)) || (a->H == 0 && (a->q_pe || a->q_pe_out))) return MLA_ERR_INVALID_VALUE;
+  if (a->kv_dtype != MLA_KV_BF16 && !a->kv_scale) return MLA_ERR_INVALID_VALUE;
+  if (a->num_pages <= 0) return MLA_ERR_INVALID_VALUE;
+  if (!aligned16(a->c) || !aligned16(a->k_pe) || !aligned16(a->q_pe) || !aligned16(a->k_pe_out) ||
+      !aligned16(a->q_pe_out) || !aligned16(a->kv_cache) || !aligned4(a->kv_scale) || !aligned4(a->block_table) ||
+      !aligned4(a->cu_seqlens) || !aligned4(a->seq_lens))
+    return MLA_ERR_MISALIGNED;
+  const int64_t strides[][2] = {{a->c_tok, a->n_tok},
+                                {a->k_pe_tok, a->n_tok},
+                                {a->k_pe_out_tok, a->k_pe_out ? a->n_tok : 0},
+                                {a->q_pe_tok, a->H > 0 ? a->n_tok : 0},
+                                {a->q_pe_head, a->H},
+                                {a->q_pe_out_tok, a->H > 0 ? a->n_tok : 0},
+                                {a->q_pe_out_head, a->H}};
+  for (const auto& s : strides)
+    if ((st = check_stride(s[0], s[1])) != MLA_OK) return st;
+  // in place means the same elements: another stride would read what was written
+  if (a->k_pe_out == a->k_pe && a->n_tok > 1 && a->k_pe_out_tok != a->k_pe_tok) return MLA_ERR_INVALID_VALUE;
+  if (a->H > 0 && a->q_pe_out == a->q_pe &&
+      ((a->n_tok > 1 && a->q_pe_out_tok != a->q_pe_tok) || (a->H > 1 && a->q_pe_out_head != a->q_pe_head)))
+    return MLA_ERR_INVALID_VALUE;
+  return from_cuda(launch_append(a, (cudaStream_t)stream));
+}
+
+mla_status_t mla_prefill_packed_workspace_size(const mla_prefill_packed_args_t* a, size_t* bytes) {
+  mla_status_t st = check_packed_shape(a);
+  if (st != MLA_OK) return st;
+  if (!bytes) return MLA_ERR_INVALID_VALUE;
+  *bytes = kStatusBytes;
+  return MLA_OK;
+}
+
+mla_status_t mla_prefill_packed(const mla_prefill_packed_args_t* a, void* stream) {
+  mla_status_t st = check_packed_shape(a);
+  if (st == MLA_OK) st = check_status_workspace(a->workspace, a->workspace_bytes);
+  if (st != MLA_OK || a->B == 0 || a->n_tok == 0) return st;
+  if (!a->q_nope || !a->k_nope || !a->v || !a->cu_seqlens || !a->out) return MLA_ERR_INVALID_VALUE;
+  if ((a->d_r > 0) != (a->q_pe != nullptr) || (a->d_r > 0) != (a->k_pe != nullptr)) return MLA_ERR_INVALID_VALUE;
+  if (!aligned16(a->q_nope) || !aligned16(a->q_pe) || !aligned16(a->k_nope) || !aligned16(a->k_pe) ||
+      !aligned16(a->v) || !aligned16(a->out) || !aligned4(a->cu_seqlens) || !aligned4(a->lse))
+    return MLA_ERR_MISALIGNED;
+  const int64_t pe_tok = a->d_r > 0 ? a->n_tok : 0;
+  const int64_t strides[][2] = {{a->q_nope_tok, a->n_tok}, {a->q_nope_head, a->H},      {a->q_pe_tok, pe_tok},
+                                {a->q_pe_head, a->d_r > 0 ? a->H : 0}, {a->k_nope_tok, a->n_tok}, {a->k_nope_head, a->H_kv},
+                                {a->k_pe_tok, pe_tok},     {a->v_tok, a->n_tok},        {a->v_head, a->H_kv}};
+  for (const auto& s : strides)
+    if ((st = check_stride(s[0], s[1])) != MLA_OK) return st;
+  return from_cuda(launch_prefill_packed(a, (cudaStream_t)stream));
+}
+
+mla_status_t mla_verify_workspace_size(const mla_verify_args_t* a, size_t* bytes) {
+  mla_status_t st = check_verify_shape(a);
+  if (st != MLA_OK) return st;
+  if (!bytes) return MLA_ERR_INVALID_VALUE;
+  *bytes = kStatusBytes;
+  return MLA_OK;
+}
+
+mla_status_t mla_verify_draft(const mla_verify_args_t* a, void* stream) {
+  mla_status_t st = check_verify_shape(a);
+  if (st == MLA_OK) st = check_status_workspace(a->workspace, a->workspace_bytes);
+  if (st != MLA_OK || a->B == 0) return st;
+  if (!a->target_probs || !a->u_sample || !a->tokens || !a->num_accepted) return MLA_ERR_INVALID_VALUE;
+  if (a->s_q > 1 && (!a->draft_tokens || !a->u_accept)) return MLA_ERR_INVALID_VALUE;
+  if (a->new_lens && !a->seq_lens) return MLA_ERR_INVALID_VALUE;
+  const uintptr_t step = a->dtype == MLA_PROB_BF16 ? 1 : 3;
+  if ((reinterpret_cast<uintptr_t>(a->target_probs) & step) || (reinterpret_cast<uintptr_t>(a->draft_probs) & step) ||
+      !aligned4(a->draft_tokens) || !aligned4(a->num_draft) || !aligned4(a->u_accept) || !aligned4(a->u_sample) ||
+      !aligned4(a->seq_lens) || !aligned4(a->tokens) || !aligned4(a->num_accepted) || !aligned4(a->new_lens))
+    return MLA_ERR_MISALIGNED;
+  if ((a->B > 1 && a->target_seq < 0) || (a->s_q > 1 && a->target_row < 0)) return MLA_ERR_INVALID_VALUE;
+  if (a->draft_probs && ((a->B > 1 && a->draft_seq < 0) || (a->s_q > 2 && a->draft_row < 0))) return MLA_ERR_INVALID_VALUE;
+  return from_cuda(launch_verify(a, (cudaStream_t)stream));
+}
+
 mla_status_t mla_get_status(void* workspace, void* stream) {
   if (!workspace) return MLA_ERR_INVALID_VALUE;
   uint32_t word = 0;
@@ -436,6 +580,7 @@ const char* mla_status_string(mla_status_t s) {
     case MLA_ERR_DEVICE_TIMEOUT: return "MLA_ERR_DEVICE_TIMEOUT";
     case MLA_ERR_BAD_BLOCK_TABLE: return "MLA_ERR_BAD_BLOCK_TABLE";
     case MLA_ERR_BAD_SEQ_LEN: return "MLA_ERR_BAD_SEQ_LEN";
+    case MLA_ERR_BAD_TOKEN: return "MLA_ERR_BAD_TOKEN";
   }
   return "MLA_ERR_UNKNOWN";
 }

@@ -5,16 +5,20 @@ form); it owns the intermediate device buffers (q_lat, o_lat, lse, out and the
 workspace) and replays the four calls on the current stream.  ``FusedStep``: the
 same step through ``mla_decode_step`` (one call; one launch where the shape
 allows).  ``PrefillStep``: the explicit form for long chunks of new tokens (one
-call, two kernels).  None does arithmetic of its own.
+call, two kernels).  ``PackedPrefill``: whole prompts of different lengths, into
+the cache and through the explicit form.  ``SpeculativeStep``: a decode step over
+drafted tokens with its append and their verification.  None does arithmetic of
+its own.
 """
 
 from __future__ import annotations
 
 import torch
 
-from . import (D_C, D_N, D_V, alloc_workspace, make_decode_args, make_prefill_args, make_step_args,
-               mla_absorb_q, mla_combine_splits, mla_decode_num_splits, mla_decode_paged,
-               mla_decode_step, mla_decode_step_launches, mla_prefill, mla_up_proj_v)
+from . import (D_C, D_N, D_R, D_V, alloc_workspace, make_append_args, make_decode_args, make_prefill_args,
+               make_prefill_packed_args, make_step_args, make_verify_args, mla_absorb_q, mla_append_kv,
+               mla_combine_splits, mla_decode_num_splits, mla_decode_paged, mla_decode_step,
+               mla_decode_step_launches, mla_prefill, mla_prefill_packed, mla_up_proj_v, mla_verify_draft)
 
 
 class DecodeStep:
@@ -160,3 +164,81 @@ def prefill_from_workload(w, device="cuda", max_seq_len=None):
                        kv_cache=d(w.kv_cache), block_table=d(w.block_table),
                        seq_lens=d(w.seq_lens), causal=w.causal, softmax_scale=w.softmax_scale,
                        max_seq_len=max_seq_len or max(max(w.lens), w.spec.s_q))
+
+
+class PackedPrefill:
+    """Whole prompts of different lengths, packed one after another: their latents
+    and rotated RoPE keys go into the paged cache, and their tokens attend to their
+    own prompt in the explicit form.  q [n_tok][H][192] and kv [n_tok][H][256] are
+    the query's and the per-head key and value up-projections' outputs, latent
+    [n_tok][576] the joint down-projection's (latent and RoPE key); nothing in them
+    is rotated yet.  seq_lens holds the prompts' lengths.  Owns out, lse, the
+    rotated parts and the workspaces."""
+
+    def __init__(self, *, q, kv, latent, kv_cache, kv_scale, block_table, cu_seqlens, seq_lens, softmax_scale,
+                 rope_base=10000.0, out=None):
+        n, H, _ = q.shape
+        dev = q.device
+        bf16 = torch.bfloat16
+        self.q_pe = torch.empty(n, H, D_R, dtype=bf16, device=dev)
+        self.k_pe = torch.empty(n, D_R, dtype=bf16, device=dev)
+        self.lse = torch.empty(n, H, dtype=torch.float32, device=dev)
+        self.out = out if out is not None else torch.empty(n, H, D_V, dtype=bf16, device=dev)
+        self.append_args = make_append_args(
+            c=latent[:, :D_C], k_pe=latent[:, D_C:], q_pe=q[..., D_N:], k_pe_out=self.k_pe, q_pe_out=self.q_pe,
+            kv_cache=kv_cache, kv_scale=kv_scale, block_table=block_table, cu_seqlens=cu_seqlens, seq_lens=seq_lens,
+            rope_base=rope_base)
+        self.attend_args = make_prefill_packed_args(
+            q_nope=q[..., :D_N], q_pe=self.q_pe, k_nope=kv[..., :D_N], k_pe=self.k_pe, v=kv[..., D_N:],
+            cu_seqlens=cu_seqlens, out=self.out, lse=self.lse, causal=True, softmax_scale=softmax_scale)
+        self.append_workspace = alloc_workspace(self.append_args)
+        self.workspace = alloc_workspace(self.attend_args)
+        self._keep = (q, kv, latent, kv_cache, kv_scale, block_table, cu_seqlens, seq_lens)
+
+    def run(self, stream=None):
+        mla_append_kv(self.append_args, stream)
+        mla_prefill_packed(self.attend_args, stream)
+        return self.out
+
+
+class SpeculativeStep(DecodeStep):
+    """One decode step over the last token and its s_q - 1 drafts of every sequence:
+    appends their latents and rotated RoPE keys (latent [B * s_q][576], q_pe
+    [B][s_q][H][64], not yet rotated), attends causally, and, once the model has
+    turned the output into probabilities, verifies the drafts; ``seq_lens`` (the
+    drafts included) then loses the rejected ones in place."""
+
+    def __init__(self, *, latent, q_nope, q_pe, w_uk, w_uv, kv_cache, kv_scale, block_table, seq_lens,
+                 softmax_scale, rope_base=10000.0, num_splits=0, max_seq_len=0, out=None):
+        B, s_q, H, _ = q_pe.shape
+        dev = q_pe.device
+        rotated = torch.empty_like(q_pe, memory_format=torch.contiguous_format)
+        super().__init__(q_nope=q_nope, q_pe=rotated, w_uk=w_uk, w_uv=w_uv, kv_cache=kv_cache, kv_scale=kv_scale,
+                         block_table=block_table, seq_lens=seq_lens, causal=True, softmax_scale=softmax_scale,
+                         num_splits=num_splits, max_seq_len=max_seq_len, out=out)
+        self.cu_seqlens = torch.arange(0, B * s_q + 1, s_q, dtype=torch.int32, device=dev)
+        self.append_args = make_append_args(
+            c=latent[:, :D_C], k_pe=latent[:, D_C:], q_pe=q_pe.flatten(0, 1), q_pe_out=rotated.flatten(0, 1),
+            kv_cache=kv_cache, kv_scale=kv_scale, block_table=block_table, cu_seqlens=self.cu_seqlens,
+            seq_lens=seq_lens, rope_base=rope_base)
+        self.append_workspace = alloc_workspace(self.append_args)
+        self.tokens = torch.empty(B, s_q, dtype=torch.int32, device=dev)
+        self.num_accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        self.seq_lens = seq_lens
+        self.verify_workspace = torch.zeros(256, dtype=torch.uint8, device=dev)
+        self._keep += (latent, q_pe)
+
+    def append(self, stream=None):
+        mla_append_kv(self.append_args, stream)
+
+    def run(self, stream=None):
+        self.append(stream)
+        return super().run(stream)
+
+    def verify(self, *, target_probs, draft_probs, draft_tokens, u_accept, u_sample, num_draft=None, stream=None):
+        args = make_verify_args(target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
+                                u_accept=u_accept, u_sample=u_sample, num_draft=num_draft, seq_lens=self.seq_lens,
+                                tokens=self.tokens, num_accepted=self.num_accepted, new_lens=self.seq_lens,
+                                workspace=self.verify_workspace)
+        mla_verify_draft(args, stream)
+        return self.tokens, self.num_accepted

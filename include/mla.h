@@ -59,7 +59,8 @@ typedef enum {
   MLA_ERR_CUDA = 5,                 /* a CUDA runtime call or launch failed */
   MLA_ERR_DEVICE_TIMEOUT = 6,       /* a bounded device wait ran out (device-side) */
   MLA_ERR_BAD_BLOCK_TABLE = 7,      /* a block-table entry outside [0, num_pages) (device-side) */
-  MLA_ERR_BAD_SEQ_LEN = 8           /* seq_lens[b] < 0 or > max_pages_per_seq*page_size (device-side) */
+  MLA_ERR_BAD_SEQ_LEN = 8,          /* seq_lens[b] < 0 or > max_pages_per_seq*page_size (device-side) */
+  MLA_ERR_BAD_TOKEN = 9             /* a drafted token outside the vocabulary (device-side) */
 } mla_status_t;
 
 /* Cache formats of a 576-value row: bf16 values; e4m3 codes with one fp32 scale
@@ -407,6 +408,182 @@ mla_status_t mla_decode_step(const mla_step_args_t* args, void* stream);
  * to bf16 rounding.  Apply it once, before the weights are used.
  */
 mla_status_t mla_fold_hadamard(void* w_dkv, int32_t d_h, void* w_uk, void* w_uv, int32_t H, void* stream);
+
+/*
+ * Packed batches (mla_append_kv, mla_prefill_packed): the tokens of B sequences
+ * of different lengths stand one after another in one array of n_tok rows.  Row
+ * t belongs to sequence b when cu_seqlens[b] <= t < cu_seqlens[b + 1]
+ * (cu_seqlens: int32 [B + 1], device, not decreasing, 0 <= cu_seqlens[0],
+ * cu_seqlens[B] <= n_tok; equal neighbours are an empty sequence).  Rows before
+ * the first and behind the last sequence have no effect, and outputs there are
+ * left as they were.  Inputs may be strided views: a *_tok stride is the distance of two rows and a *_head
+ * stride that of two heads, in values, positive multiples of 8 (a stride along a
+ * dimension of one is ignored); the innermost values are contiguous, pointers 16-byte aligned.
+ * So a query [n_tok][H][128 + 64] or an up-projection's output [n_tok][H][128 + 128]
+ * goes in as two views without a copy.
+ */
+
+/*
+ * Arguments of mla_append_kv / mla_append_workspace_size.
+ * Zero-initialise the struct, then fill every field.
+ */
+typedef struct {
+  const void* c;                  /* bf16 [n_tok][d_c], strided: the new tokens' latents */
+  const void* k_pe;               /* bf16 [n_tok][d_r], strided: their RoPE keys, not yet rotated */
+  const void* q_pe;               /* bf16 [n_tok][H][d_r], strided: the queries' RoPE parts, not yet
+                                     rotated; NULL with H = 0 */
+  void* k_pe_out;                 /* bf16 [n_tok][d_r], strided, written: the rotated keys; may be
+                                     k_pe itself (same strides) or NULL */
+  void* q_pe_out;                 /* bf16 [n_tok][H][d_r], strided, written: the rotated queries; may
+                                     be q_pe itself (same strides) */
+  void* kv_cache;                 /* as in mla_write_kv_args_t */
+  void* kv_scale;                 /* as in mla_write_kv_args_t */
+  const int32_t* block_table;     /* int32 [B][max_pages_per_seq] */
+  const int32_t* cu_seqlens;      /* int32 [B + 1], device */
+  const int32_t* seq_lens;        /* int32 [B], device: lengths including the new tokens */
+  void* workspace;                /* device, >= mla_append_workspace_size() bytes, 16-byte aligned;
+                                     its first 16 bytes must be zero before the first use (they hold
+                                     the sticky status word) */
+  size_t workspace_bytes;
+  int64_t c_tok, k_pe_tok, q_pe_tok, q_pe_head;            /* strides, in values */
+  int64_t k_pe_out_tok, q_pe_out_tok, q_pe_out_head;
+  int32_t n_tok, B, H;            /* H 0 .. 128 */
+  int32_t d_c, d_r, page_size;
+  int32_t num_pages;
+  int32_t max_pages_per_seq;
+  int32_t kv_dtype;               /* mla_kv_dtype_t */
+  float rope_base;
+} mla_append_args_t;
+
+/* Bytes of workspace mla_append_kv needs (host only): its status word's 256. */
+mla_status_t mla_append_workspace_size(const mla_append_args_t* args, size_t* bytes);
+
+/*
+ * mla_append_kv — appends new tokens whose latent and RoPE key an engine has
+ * already projected (and normalised) to the paged cache, and applies the
+ * position rotation on the way: to the key, which goes into the cache beside the
+ * latent, and to the RoPE part of the tokens' queries, which every attention
+ * entry point here takes rotated.  With n_b = cu_seqlens[b + 1] - cu_seqlens[b],
+ * row t of sequence b sits at position pos = seq_lens[b] - n_b + t - cu_seqlens[b]
+ * (row pos % page_size of page block_table[b][pos / page_size]), and
+ *   R(x)_(2i)     = x_(2i) cos(pos f_i) - x_(2i+1) sin(pos f_i)
+ *   R(x)_(2i + 1) = x_(2i) sin(pos f_i) + x_(2i+1) cos(pos f_i),  f_i = rope_base^(-2i/d_r)
+ *   cache row = c || R(k_pe),  k_pe_out = R(k_pe),  q_pe_out = R(q_pe)
+ * The rotation is computed in fp32 from an angle reduced in fp64 and rounded
+ * once: to bf16 (outputs, bf16 cache) or to the cache's codes and scales exactly
+ * as mla_write_kv states them (the key's values enter them unrounded).  The same
+ * pairing as mla_write_kv.  A page that takes new rows belongs to one sequence.
+ * A length below n_b or beyond the block table, or cu_seqlens out of order
+ * (MLA_ERR_BAD_SEQ_LEN), or a page id outside the cache (MLA_ERR_BAD_BLOCK_TABLE)
+ * is recorded in the workspace's status word and the token is skipped, its
+ * outputs included.  Gives no early start to the kernels enqueued after it.
+ */
+mla_status_t mla_append_kv(const mla_append_args_t* args, void* stream);
+
+/*
+ * Arguments of mla_prefill_packed / mla_prefill_packed_workspace_size.
+ * Zero-initialise the struct, then fill every field.
+ */
+typedef struct {
+  const void* q_nope;             /* bf16 [n_tok][H][d_n], strided */
+  const void* q_pe;               /* bf16 [n_tok][H][d_r], strided, RoPE already applied; NULL when
+                                     d_r = 0 */
+  const void* k_nope;             /* bf16 [n_tok][H_kv][d_n], strided */
+  const void* k_pe;               /* bf16 [n_tok][d_r], strided, rotated, shared by all heads; NULL
+                                     when d_r = 0 */
+  const void* v;                  /* bf16 [n_tok][H_kv][d_v], strided */
+  const int32_t* cu_seqlens;      /* int32 [B + 1], device */
+  void* out;                      /* bf16 [n_tok][H][d_v], dense, written */
+  float* lse;                     /* fp32 [n_tok][H], natural log, written; may be NULL */
+  void* workspace;                /* device, >= mla_prefill_packed_workspace_size() bytes, 16-byte
+                                     aligned; its first 16 bytes must be zero before the first use
+                                     (they hold the sticky status word) */
+  size_t workspace_bytes;
+  int64_t q_nope_tok, q_nope_head, q_pe_tok, q_pe_head;    /* strides, in values */
+  int64_t k_nope_tok, k_nope_head, k_pe_tok, v_tok, v_head;
+  int32_t n_tok, B, H, H_kv;      /* H 1 .. 128, H_kv divides H */
+  int32_t d_n, d_r, d_v;          /* d_n = d_v = 128, d_r = 64 or 0 */
+  int32_t causal;                 /* 1: a token sees its sequence up to itself; 0: all of it */
+  float softmax_scale;            /* positive; e.g. 1/sqrt(d_n + d_r) */
+} mla_prefill_packed_args_t;
+
+/* Bytes of workspace mla_prefill_packed needs (host only): its status word's 256. */
+mla_status_t mla_prefill_packed_workspace_size(const mla_prefill_packed_args_t* args, size_t* bytes);
+
+/*
+ * mla_prefill_packed — attention of whole prompts in the explicit form, before
+ * or beside their way into the cache: packed sequences of different lengths,
+ * per-head keys and values as the up-projections leave them, query heads in
+ * groups of H / H_kv that share a key and value head (head h uses
+ * g = h / (H / H_kv)).  For token i and the tokens j of its own sequence
+ * (j <= i when causal):
+ *   s_ij = softmax_scale * (q_nope_i[h] . k_nope_j[g] + q_pe_i[h] . k_pe_j)
+ *   out_i[h] = sum_j softmax(s_i)_j v_j[g],   lse_i[h] = log sum_j exp(s_ij)
+ * d_r = 64 is MLA's explicit form, d_r = 0 attention of grouped heads of width
+ * 128 without the separate RoPE part.  Scores, softmax statistics and outputs
+ * are held in fp32, the softmax weights are rounded to bf16 for the product with
+ * v, the output once to bf16.  A token that is not seen has no effect, whatever
+ * its values (infinities and NaN included).  out must not overlap an input.
+ * cu_seqlens out of order (MLA_ERR_BAD_SEQ_LEN) goes to the workspace's status
+ * word; what the rows of such a batch then hold is not defined.
+ */
+mla_status_t mla_prefill_packed(const mla_prefill_packed_args_t* args, void* stream);
+
+/* Types of mla_verify_draft's probabilities. */
+typedef enum { MLA_PROB_FP32 = 0, MLA_PROB_BF16 = 1 } mla_prob_dtype_t;
+
+/*
+ * Arguments of mla_verify_draft / mla_verify_workspace_size.
+ * Zero-initialise the struct, then fill every field.
+ */
+typedef struct {
+  const void* target_probs;       /* [B][s_q][V], strided rows: the target's probabilities after the
+                                     last accepted token (row 0) and after each draft */
+  const void* draft_probs;        /* [B][s_q - 1][V], strided rows: those each draft was drawn from;
+                                     NULL: every draft was certain (probability 1) */
+  const int32_t* draft_tokens;    /* int32 [B][s_q - 1] */
+  const int32_t* num_draft;       /* int32 [B], 0 .. s_q - 1 drafts of each sequence; NULL: s_q - 1 */
+  const float* u_accept;          /* fp32 [B][s_q - 1], random numbers in [0, 1) */
+  const float* u_sample;          /* fp32 [B], random numbers in [0, 1) */
+  const int32_t* seq_lens;        /* int32 [B]: cached tokens, the drafts included; NULL without
+                                     new_lens */
+  int32_t* tokens;                /* int32 [B][s_q], written: the accepted drafts, the token drawn
+                                     after them, then -1 */
+  int32_t* num_accepted;          /* int32 [B], written */
+  int32_t* new_lens;              /* int32 [B], written: cached tokens without the rejected drafts;
+                                     may be seq_lens itself or NULL */
+  void* workspace;                /* device, >= mla_verify_workspace_size() bytes, 16-byte aligned;
+                                     its first 16 bytes must be zero before the first use (they hold
+                                     the sticky status word) */
+  size_t workspace_bytes;
+  int64_t target_seq, target_row; /* strides of target_probs, in values */
+  int64_t draft_seq, draft_row;   /* strides of draft_probs */
+  int32_t B, s_q, V;              /* s_q 1 .. MLA_MAX_S_Q (s_q - 1 drafts) */
+  int32_t dtype;                  /* mla_prob_dtype_t of both */
+} mla_verify_args_t;
+
+/* Bytes of workspace mla_verify_draft needs (host only): its status word's 256. */
+mla_status_t mla_verify_workspace_size(const mla_verify_args_t* args, size_t* bytes);
+
+/*
+ * mla_verify_draft — the acceptance step of speculative decoding, after the s_q
+ * query tokens of mla_decode_paged have given the target's probabilities: the
+ * tokens it returns are distributed as if the target had drawn them one by one
+ * (rejection sampling against the drafting distribution).  For sequence b with n
+ * drafts x_0 .. x_(n-1), target rows p_0 .. p_n and draft rows q_0 .. q_(n-1):
+ *   a = the first i with not (u_accept_i q_i(x_i) < p_i(x_i)), or n
+ *   w_j = max(p_a(j) - q_a(j), 0) when a < n (p_a(j) where no w_j is positive), else p_n(j)
+ *   next token = the smallest j with w_0 + .. + w_j > u_sample (w_0 + .. + w_(V-1))
+ * num_accepted = a, tokens = x_0 .. x_(a-1), next, -1 .., new_lens = seq_lens - (n - a).
+ * Differences, sums and comparisons are in fp64, so the result does not depend on
+ * the order of summation but for u within some 1e-15 of a boundary.  A weight
+ * that is not positive (or NaN) counts as zero; the next token is -1 when nothing
+ * is left or the sum is not finite.  A draft outside [0, V) (MLA_ERR_BAD_TOKEN)
+ * or num_draft outside [0, s_q - 1] (MLA_ERR_BAD_SEQ_LEN) is recorded in the
+ * workspace's status word and that sequence gets num_accepted = 0, tokens = -1
+ * and new_lens = seq_lens.
+ */
+mla_status_t mla_verify_draft(const mla_verify_args_t* args, void* stream);
 
 /* Waits for `stream`, returns the sticky device status word of `workspace`
  * (MLA_OK if no device-side problem was recorded) and clears it. */

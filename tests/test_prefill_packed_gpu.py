@@ -1,0 +1,269 @@
+"""GPU parity of the packed prompt attention (mla_prefill_packed) against the fp64
+oracle.
+
+Tolerances, per row and head, from the exact quantities A = sum_j p_j |v_j| and
+S = max_j softmax_scale sum_d |q_d k_jd|: an fp32 score is off by at most
+d = 192 2^-23 S (192 products summed in fp32, in any order, and the scale), which
+moves every p_j by the factor exp(2 d) at most, some 2.1 d of it; the exponential itself is off
+by at most 2^-16 of its value; p is rounded to bf16 for the product with v (2^-8 of
+it) and the output to bf16 (2^-8 of it).  So |o| is off by at most
+(2^-8 + 2.1 d + 2^-15) A + 2^-8 |o|, and lse by d + 2^-15 + 2^-21 |lse|.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from mla_inputs import bf16_bits
+from oracle import mla_oracle as om
+from oracle import serving
+
+from parity_util import to_np
+
+pytestmark = pytest.mark.gpu
+
+bf16, i32 = torch.bfloat16, torch.int32
+
+
+def make(lens, H, H_kv, d_r, seed=1, head=0, tail=0, fused=True, gain=1.0):
+    """Packed inputs on the GPU; `fused`: views of the projections' outputs."""
+    g = torch.Generator().manual_seed(seed)
+    n = head + sum(lens) + tail
+    r = lambda *s: (torch.randn(*s, generator=g) * gain).to(bf16).cuda()
+    if fused and d_r:
+        q, kv, lat = r(n, H, 192), r(n, H_kv, 256), r(n, 576)
+        x = dict(q_nope=q[..., :128], q_pe=q[..., 128:], k_nope=kv[..., :128], k_pe=lat[:, 512:], v=kv[..., 128:])
+    elif fused:
+        t = r(n, H + 2 * H_kv, 128)
+        x = dict(q_nope=t[:, :H], q_pe=None, k_nope=t[:, H:H + H_kv], k_pe=None, v=t[:, H + H_kv:])
+    else:
+        # heads outermost
+        x = dict(q_nope=r(H, n, 128).transpose(0, 1), q_pe=r(H, n, d_r).transpose(0, 1) if d_r else None,
+                 k_nope=r(H_kv, n, 128).transpose(0, 1), k_pe=r(n, d_r) if d_r else None,
+                 v=r(H_kv, n, 128).transpose(0, 1))
+    x["cu_seqlens"] = torch.tensor([head] + list(head + np.cumsum(lens)), dtype=i32).cuda()
+    x["out"] = torch.full((n, H, 128), 7.0, dtype=bf16, device="cuda")
+    x["lse"] = torch.full((n, H), 7.0, device="cuda")
+    return x
+
+
+def run(mla, x, causal=True, scale=None, stream=None):
+    scale = scale or 1.0 / (192 if x["q_pe"] is not None else 128) ** 0.5
+    a = mla.make_prefill_packed_args(**x, causal=causal, softmax_scale=scale)
+    ws = mla.alloc_workspace(a)
+    mla.mla_prefill_packed(a, stream)
+    status = mla.mla_get_status(ws, stream)
+    torch.cuda.synchronize()
+    return status
+
+
+def f64(t):
+    return om.bf16_to_f64(bf16_bits(t.cpu().contiguous()))
+
+
+def oracle_of(x, causal, scale=None):
+    q, k, v = f64(x["q_nope"]), f64(x["k_nope"]), f64(x["v"])
+    scale = scale or 1.0 / (192 if x["q_pe"] is not None else 128) ** 0.5
+    if x["q_pe"] is not None:
+        q = np.concatenate([q, f64(x["q_pe"])], -1)
+        k = np.concatenate([k, np.repeat(f64(x["k_pe"])[:, None], k.shape[1], 1)], -1)
+    return serving.attend_packed(q, k, v, x["cu_seqlens"].cpu().numpy(), scale, causal)
+
+
+def check(x, ref, rows=None):
+    o, lse, mass, size = ref
+    got, got_lse = to_np(x["out"]), to_np(x["lse"])
+    real = ~np.isnan(lse[:, 0]) if rows is None else rows
+    d = 192 * 2.0 ** -23 * size[real]
+    off = np.abs(got[real] - o[real])
+    tol = (2.0 ** -8 + 2.1 * d + 2.0 ** -15)[..., None] * mass[real] + 2.0 ** -8 * np.abs(o[real])
+    assert (off <= tol).all(), (float((off / np.maximum(tol, 1e-30)).max()), np.argwhere(off > tol)[:3])
+    off = np.abs(got_lse[real] - lse[real])
+    assert (off <= d + 2.0 ** -15 + 2.0 ** -21 * np.abs(lse[real])).all(), float(off.max())
+
+
+def untouched(x):
+    cu = x["cu_seqlens"].tolist()
+    for t in (x["out"], x["lse"]):
+        assert bool((t[:cu[0]] == 7).all()) and bool((t[cu[-1]:] == 7).all())
+
+
+CASES = [
+    # lens, H, H_kv, d_r, extra
+    ([1], 1, 1, 64, {}),
+    ([1], 16, 2, 0, {}),
+    ([17], 16, 16, 64, {}),
+    ([1, 0, 2, 0, 0, 5], 4, 4, 64, dict(head=3, tail=4)),            # empty sequences, rows of none
+    ([127, 128, 129], 2, 2, 64, {}),                                 # about a key tile
+    ([255, 256, 257], 2, 1, 0, dict(tail=1)),                        # about a query block
+    ([3, 130, 300, 64, 1, 200], 4, 4, 64, {}),                       # boundaries inside tiles
+    ([3, 130, 300, 64, 1, 200], 8, 2, 0, dict(fused=False)),         # grouped, heads outermost
+    ([600], 3, 3, 64, dict(fused=False)),                            # an odd number of heads
+    ([512], 6, 2, 64, {}),                                           # grouped heads with the shared key
+    ([40] * 30, 2, 2, 64, dict(tail=9)),                             # many sequences in a tile
+    ([1] * 300, 1, 1, 0, {}),                                        # one token each
+    ([200, 77], 2, 2, 64, dict(gain=6.0)),                           # peaked softmax, large scores
+]
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,H,H_kv,d_r,kw", CASES)
+def test_packed_matches_oracle(cuda_lib, lens, H, H_kv, d_r, kw, causal):
+    x = make(lens, H, H_kv, d_r, **kw)
+    assert run(cuda_lib, x, causal) == 0
+    check(x, oracle_of(x, causal))
+    untouched(x)
+
+
+def test_packed_long_sampled(cuda_lib):
+    """A long prompt between short ones: sampled rows against the definition."""
+    lens = [5, 5000, 300]
+    x = make(lens, 4, 2, 64, seed=3)
+    assert run(cuda_lib, x) == 0
+    q = torch.cat([x["q_nope"], x["q_pe"]], -1).cpu()
+    k = torch.cat([x["k_nope"], x["k_pe"][:, None].expand(-1, 2, -1)], -1).cpu()
+    v, rows = x["v"].cpu(), [4, 5, 132, 133, 1000, 2600, 4999, 5004, 5005, 5304]
+    n = sum(lens)
+    o, lse = np.full((n, 4, 128), np.nan), np.full((n, 4), np.nan)
+    mass, size = o.copy(), lse.copy()
+    cu = [0, 5, 5005, 5305]
+    for t in rows:
+        lo = max(c for c in cu if c <= t)
+        got = one_row(q[t], k[lo:t + 1], v[lo:t + 1])
+        o[t], lse[t], mass[t], size[t] = (a[-1] for a in got)
+    check(x, (o, lse, mass, size))
+
+
+def one_row(q, k, v):
+    """The last row of a causal prompt."""
+    q, k, v = f64(q), f64(k), f64(v)
+    out = []
+    for h in range(q.shape[0]):
+        kk, vv = k[:, h // 2], v[:, h // 2]
+        s = kk @ q[h] / 192 ** 0.5
+        p = np.exp(s - s.max())
+        out.append(((p / p.sum()) @ vv, s.max() + np.log(p.sum()), (p / p.sum()) @ np.abs(vv),
+                    (np.abs(kk) @ np.abs(q[h])).max() / 192 ** 0.5))
+    return [np.stack([o[i] for o in out])[None] for i in range(4)]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_packed_unseen_values_have_no_effect(cuda_lib, bad):
+    """NaN and infinities in tokens that a row does not see: later tokens of its
+    prompt, other prompts, rows of no prompt.  Rows that see them are not compared."""
+    lens = [130, 90, 200]
+    x = make(lens, 2, 2, 64, seed=4, head=1, tail=30)
+    ref = oracle_of(x, True)
+    spoilt = [0, 100, 131, 220, 400, 421, 425, 450]
+    for t in spoilt:
+        for name in ("k_nope", "k_pe", "v"):
+            x[name][t] = bad
+    x["q_nope"][425:] = bad
+    assert run(cuda_lib, x) == 0
+    cu = [1, 131, 221, 421]
+    good = np.zeros(sum(lens) + 31, bool)
+    for lo, hi in zip(cu, cu[1:]):
+        stop = min([t for t in spoilt if lo <= t < hi] + [hi])
+        good[lo:stop] = True
+    check(x, ref, good)
+    untouched(x)
+    # rows that see one hold what the definition gives there: not a number for NaN
+    if bad != bad:
+        assert bool(torch.isnan(x["out"][100]).all()) and bool(torch.isnan(x["out"][130]).all())
+
+
+def test_packed_one_bad_query_stays_alone(cuda_lib):
+    x = make([300], 2, 2, 64, seed=5)
+    ref = oracle_of(x, True)
+    x["q_nope"][77] = float("nan")
+    assert run(cuda_lib, x) == 0
+    good = np.ones(300, bool)
+    good[77] = False
+    check(x, ref, good)
+    assert bool(torch.isnan(x["out"][77]).all())
+
+
+def test_packed_all_scores_minus_infinity(cuda_lib):
+    """A row whose every score is -inf weighs nothing: zeros and lse = -inf."""
+    x = make([3], 2, 2, 0, seed=6)
+    x["q_nope"].fill_(1.0)
+    x["k_nope"].fill_(1.0)
+    x["k_nope"][0, :, 0] = -float("inf")
+    assert run(cuda_lib, x) == 0
+    assert bool((x["out"][0] == 0).all()) and bool(torch.isneginf(x["lse"][0]).all())
+    assert bool(torch.isfinite(x["lse"][1:]).all())
+
+
+def test_packed_without_lse_repeats_and_replays(cuda_lib):
+    """Bit-identical again, on another stream, and replayed from a graph with other
+    offsets in place."""
+    x = make([100, 300, 57], 4, 4, 64, seed=7)
+    assert run(cuda_lib, x) == 0
+    first, lse = x["out"].clone(), x["lse"].clone()
+    x["out"].fill_(7)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    assert run(cuda_lib, x, stream=s) == 0
+    assert torch.equal(first, x["out"]) and torch.equal(lse, x["lse"])
+    x["lse"] = None
+    x["out"].fill_(7)
+    a = cuda_lib.make_prefill_packed_args(**x, causal=True, softmax_scale=1 / 192 ** 0.5)
+    ws = cuda_lib.alloc_workspace(a)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cuda_lib.mla_prefill_packed(a)
+    g.replay()
+    assert cuda_lib.mla_get_status(ws) == 0 and torch.equal(first, x["out"])
+    x["cu_seqlens"][1] = 40
+    g.replay()
+    assert cuda_lib.mla_get_status(ws) == 0
+    got = x["out"].clone()
+    x["lse"] = torch.empty(457, 4, device="cuda")
+    assert run(cuda_lib, x) == 0
+    assert torch.equal(got, x["out"])
+
+
+def test_packed_bad_offsets_are_reported(cuda_lib):
+    x = make([50, 50], 2, 2, 64, seed=8)
+    x["cu_seqlens"][1] = 120
+    assert run(cuda_lib, x) == 8
+
+
+def test_packed_prefill_agrees_with_the_cached_form(cuda_lib):
+    """Prompts appended to the cache and attended there in the explicit form give what
+    the packed attention gives on the same up-projected keys and values."""
+    from head_latent_attention_06_b200.step import PackedPrefill, PrefillStep
+    g = torch.Generator().manual_seed(9)
+    r = lambda *s: torch.randn(*s, generator=g)
+    L, B, H = 192, 2, 16
+    n = B * L
+    latent = r(n, 576).to(bf16).cuda()
+    q = r(n, H, 192).to(bf16).cuda()
+    w_uk, w_uv = ((r(H, 128, 512) / 512 ** 0.5).to(bf16).cuda() for _ in range(2))
+    c = latent[:, :512].double()
+    kv = torch.cat([torch.einsum("tc,hnc->thn", c, w.double()) for w in (w_uk, w_uv)], -1).to(bf16)
+    cache = torch.zeros(8, 64, 576, dtype=bf16, device="cuda")
+    table = torch.tensor([[5, 0, 3], [1, 7, 2]], dtype=i32, device="cuda")
+    lens = torch.tensor([L, L], dtype=i32, device="cuda")
+    cu = torch.tensor([0, L, 2 * L], dtype=i32, device="cuda")
+    scale = 1 / 192 ** 0.5
+    step = PackedPrefill(q=q, kv=kv, latent=latent, kv_cache=cache, kv_scale=None, block_table=table, cu_seqlens=cu,
+                         seq_lens=lens, softmax_scale=scale)
+    step.run()
+    assert cuda_lib.mla_get_status(step.workspace) == 0 and cuda_lib.mla_get_status(step.append_workspace) == 0
+    ref = PrefillStep(q_nope=q[..., :128].reshape(B, L, H, 128).contiguous(), q_pe=step.q_pe.view(B, L, H, 64), w_uk=w_uk,
+                      w_uv=w_uv, kv_cache=cache, block_table=table, seq_lens=lens, causal=True, softmax_scale=scale,
+                      max_seq_len=L)
+    ref.run()
+    assert cuda_lib.mla_get_status(ref.workspace) == 0
+    x = dict(q_nope=q[..., :128], q_pe=step.q_pe, k_nope=kv[..., :128], k_pe=step.k_pe, v=kv[..., 128:], cu_seqlens=cu,
+             out=step.out, lse=step.lse)
+    want = oracle_of(x, True)
+    check(x, want)
+    # the cached form rounds the same keys and values from fp32 sums: a whole bf16 step
+    # (2^-7) where the sum falls the other way, in a score and in v, besides each side's
+    # own tolerance
+    d = 192 * 2.0 ** -23 * want[3] + 2.0 ** -7 * want[3]
+    tol = 2 * ((2.0 ** -8 + 2.1 * d + 2.0 ** -15)[..., None] * want[2] + 2.0 ** -8 * np.abs(want[0])) + 2.0 ** -7 * want[2]
+    assert (np.abs(to_np(step.out) - to_np(ref.out).reshape(n, H, 128)) <= tol).all()
