@@ -222,7 +222,10 @@ def test_oracle_verification_draws_from_the_target():
                 t, a, new = serving.verify_draft(p, q, [[x]], [1], [[u]], [r], [7])
                 assert new[0] == 6 + a[0]
                 share[t[0, 0]] += q[0, 0, x] / (n * len(grid[::8]))
-    assert np.abs(share - p[0, 0]).max() < 0.02
+    # a draft's accepted share is off by less than one of the 200 points (weighted by
+    # q <= 0.6); of the rejected 0.6 = sum max(p - q, 0), a token's share lies between two
+    # boundaries, each off by less than one of the 25 points
+    assert np.abs(share - p[0, 0]).max() < 0.6 / 200 + 2 * 0.6 / 25
 
 
 def test_oracle_append_positions():
