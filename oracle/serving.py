@@ -60,6 +60,7 @@ def attend_packed(q, k, v, cu, scale, causal):
 def verify_draft(p, q, draft, num, u_accept, u_sample, seq_lens):
     """(tokens, accepted, new_lens); p [B][S + 1][V], q [B][S][V] or None."""
     B, rows, V = p.shape
+    draft, u_accept = np.asarray(draft), np.asarray(u_accept)
     tokens = np.full((B, rows), -1, np.int64)
     accepted, new_lens = np.zeros(B, np.int64), np.array(seq_lens, np.int64)
     for b in range(B):
