@@ -3,9 +3,17 @@
 #include <math_constants.h>
 
 #include "packed.cuh"
+#include "sm100.cuh"
+#include "tma_host.cuh"
 
 namespace mla {
+uint64_t device_wait_limit_ns();
+
 namespace {
+
+using namespace sm100;
+
+constexpr uint64_t kDrainNs = 100000000ull;
 
 struct PackedParams {
   const __nv_bfloat16* q_nope;
@@ -18,8 +26,9 @@ struct PackedParams {
   float* lse;
   uint32_t* status;
   int64_t qn_tok, qn_head, qp_tok, qp_head, kn_tok, kn_head, kp_tok, v_tok, v_head;
-  int n_tok, B, H, share, causal;
+  int n_tok, B, H, share, causal, blocks;
   float scale_log2;
+  uint64_t wait_ns;
 };
 
 MLA_DEVI float dot8(const uint4& a, const uint4& b, float acc) {
@@ -87,18 +96,477 @@ MLA_DEVI void attend_row(const PackedParams& p, int t, int h, int lo, int hi, in
   if (p.lse && lane == 0) p.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * 0.6931471805599453f;
 }
 
+// ---------------------------------------------------------------- tiles
+constexpr int kThreads = 384;               // warp 0 loads, warp 1 MMA, warps 4..7 tile A, 8..11 tile B
+constexpr int kRows = 256;                  // packed rows of a CTA: tile A the first 128, B the others
+constexpr uint32_t kChunk = 128 * 128;      // 16 KB: 128 rows x 64 values, or 64 keys x 128 values
+constexpr int kHeadGroup = 8;               // heads whose blocks run side by side
+
 template <bool PE>
-__global__ void __launch_bounds__(128) packed_rows_kernel(const PackedParams p) {
+struct Cfg {
+  static constexpr int kQk = PE ? 3 : 2;              // 64-value chunks of a query or key
+  static constexpr int kSlots = PE ? 8 : 10;          // ring of K and V chunks
+  static constexpr int kPer = kQk + 2;                // chunks of one key tile: K, then V in halves of 64 keys
+  static constexpr uint32_t kRing = 2 * kQk * kChunk;
+  static constexpr uint32_t kBars = kRing + kSlots * kChunk;
+  static constexpr uint32_t kSmem = kBars + 512 + 1024;
+};
+static_assert(Cfg<true>::kSmem <= 232448 && Cfg<false>::kSmem <= 232448, "shared memory budget");
+
+// TMEM: scores (and the weights over them) of tile t at columns 128 t, outputs at 256 + 128 t
+constexpr uint32_t kTmemO = 256;
+constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
+constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
+constexpr float kRescale = 8.0f;
+// barriers; [2] per tile, P[2 t + half]
+constexpr int B_Q = 0, B_S = 1, B_P = 3, B_O = 7, B_DRAIN = 9, B_FULL = 10;
+
+struct Tiles {
+  int k0;         // first key of the block's first key tile
+  int n;          // key tiles
+  int from[2], to[2];  // those of them that query tile A and B see
+};
+
+// 2^x by a polynomial on the FMA pipe: x = n + f, |f| <= 1/2, 2^f by the degree-4
+// minimax polynomial of relative error 2.6e-6 (its coefficients come out of a Remez
+// exchange), the exponent n added to the bits.  For finite x >= -126.
+MLA_DEVI uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+MLA_DEVI void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+MLA_DEVI uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+MLA_DEVI uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+MLA_DEVI void exp2_poly2(uint64_t x, float& p0, float& p1) {
+  float x0, x1;
+  unpack2(x, x0, x1);
+  x = pack2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves round(x) in the low mantissa bits
+  const uint64_t t = add2(x, pack2(kMagic, kMagic));
+  const uint64_t f = add2(x, add2(pack2(kMagic, kMagic), t ^ 0x8000000080000000ull));  // x - (t - magic)
+  uint64_t r = pack2(0.009570102207362652f, 0.009570102207362652f);
+  r = fma2(r, f, pack2(0.05591785907745361f, 0.05591785907745361f));
+  r = fma2(r, f, pack2(0.240247443318367f, 0.240247443318367f));
+  r = fma2(r, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+  r = fma2(r, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  unpack2(r, p0, p1);
+  float t0, t1;
+  unpack2(t, t0, t1);
+  p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+// maximum of three that keeps a NaN
+MLA_DEVI float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+template <bool PE>
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_attn_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qp,
+                       const __grid_constant__ CUtensorMap tm_kn, const __grid_constant__ CUtensorMap tm_kp,
+                       const __grid_constant__ CUtensorMap tm_v, const PackedParams p) {
+  using C = Cfg<PE>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sa = (raw + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (sa - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) -> uint32_t { return sa + C::kBars + 8u * i; };
+  auto full = [&](int s) -> uint32_t { return bar(B_FULL + s); };
+  auto empty = [&](int s) -> uint32_t { return bar(B_FULL + C::kSlots + s); };
+  int* words = reinterpret_cast<int*>(sm + C::kBars + 8 * (B_FULL + 2 * C::kSlots));
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
+  volatile int* abort_flag = words + 1;
+  int* issued = words + 2;
+  int* low = words + 4;    // [8] per softmax warp: the first key its rows see
+  int* high = words + 12;  // [8] one past the last
+
+  // blocks of a group of heads in turn, the last rows (the longest, when causal) first
+  const int per_group = kHeadGroup * p.blocks;
+  const int grp = blockIdx.x / per_group, in = blockIdx.x - grp * per_group;
+  const int gh = min(kHeadGroup, p.H - grp * kHeadGroup);
+  const int blk = p.blocks - 1 - in / gh, h = grp * kHeadGroup + in % gh;
+  const int g = h / p.share;
+  const int q0 = blk * kRows;
+  const uint64_t wait_ns = p.wait_ns;
+
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    *issued = 0;
+    mbar_init(bar(B_Q), 1);
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(bar(B_S + t), 1);
+      mbar_init(bar(B_P + 2 * t), 4);
+      mbar_init(bar(B_P + 2 * t + 1), 4);
+      mbar_init(bar(B_O + t), 1);
+    }
+    mbar_init(bar(B_DRAIN), 1);
+    for (int s = 0; s < C::kSlots; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc_1(smem_u32(tmem_slot), 512);
+    tmem_relinquish_1();
+  }
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  if (blockIdx.x == 0) packed_check(p.cu, p.B, p.n_tok, p.status, threadIdx.x, 128);
-  const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int t = (int)(w / p.H), h = (int)(w % p.H);
-  if (t >= p.n_tok) return;
-  const PackedSeq s = packed_find(p.cu, p.B, p.n_tok, t, lane);
-  if (s.b < 0) return;
-  attend_row<PE>(p, t, h, s.lo, p.causal ? t + 1 : s.hi, lane);
+  // ---- the keys of every row: of its own prompt, up to itself when causal
+  const int t = (warp - 4) >> 2;                          // query tile of a softmax warp
+  const int row = 32 * (warp & 3) + lane;                 // its TMEM lane
+  const int qi = q0 + 128 * t + row;
+  int lo = 0, hi = 0;
+  if (warp >= 4) {
+    const int first = q0 + 128 * t + 32 * (warp & 3);
+    if (first < p.n_tok) {
+      const PackedRow r = packed_row(p.cu, p.B, p.n_tok, first, lane);
+      lo = r.lo;
+      hi = r.hi;
+      if (p.causal && hi > lo) hi = qi + 1;
+    }
+    const int a = __reduce_min_sync(0xffffffffu, hi > lo ? lo : 0x7fffffff);
+    const int z = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      low[warp - 4] = a;
+      high[warp - 4] = z;
+    }
+  } else if (blockIdx.x == 0 && warp >= 2) {
+    packed_check(p.cu, p.B, p.n_tok, p.status, threadIdx.x - 64, 64);
+  } else if (warp == 0 && lane == 0) {
+    // both tiles' queries (rows past the end read as zeros)
+    mbar_arrive_expect_tx_local(bar(B_Q), 2 * C::kQk * kChunk);
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t dst = sa + i * C::kQk * kChunk;
+      tma_load_3d_cta(dst, &tm_qn, bar(B_Q), 0, h, q0 + 128 * i);
+      tma_load_3d_cta(dst + kChunk, &tm_qn, bar(B_Q), 64, h, q0 + 128 * i);
+      if constexpr (PE) tma_load_3d_cta(dst + 2 * kChunk, &tm_qp, bar(B_Q), 0, h, q0 + 128 * i);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  Tiles T;
+  {
+    int a[2], z[2];
+    for (int i = 0; i < 2; ++i) {
+      a[i] = min(min(low[4 * i], low[4 * i + 1]), min(low[4 * i + 2], low[4 * i + 3]));
+      z[i] = max(max(high[4 * i], high[4 * i + 1]), max(high[4 * i + 2], high[4 * i + 3]));
+    }
+    T.k0 = min(a[0], a[1]);
+    T.n = 0;
+    for (int i = 0; i < 2; ++i) {
+      const bool any = z[i] > a[i];
+      T.from[i] = any ? (a[i] - T.k0) / 128 : 0;
+      T.to[i] = any ? (z[i] - T.k0 + 127) / 128 : 0;
+      T.n = max(T.n, T.to[i]);
+    }
+  }
+
+  if (warp == 0) {
+    // =========================== loads ===========================
+    // K chunks of a tile, then its V in halves of 64 keys, round the ring
+    int s = 0, ph = 1, count = 0;
+    bool ok = true;
+    for (int j = 0; ok && j < T.n; ++j) {
+      const int key = T.k0 + 128 * j;
+#pragma unroll
+      for (int c = 0; c < C::kPer; ++c) {
+        ok = ok && mbar_wait_converged(empty(s), ph, abort_flag, p.status, wait_ns);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t dst = sa + C::kRing + s * kChunk;
+          mbar_arrive_expect_tx_local(full(s), kChunk);
+          if (c < 2) {
+            tma_load_3d_cta(dst, &tm_kn, full(s), 64 * c, g, key);
+          } else if (PE && c == 2) {
+            tma_load_3d_cta(dst, &tm_kp, full(s), 0, 0, key);
+          } else {
+            const int k = key + 64 * (c - C::kQk);
+            tma_load_3d_cta(dst, &tm_v, full(s), 0, g, k);
+            tma_load_3d_cta(dst + kChunk / 2, &tm_v, full(s), 64, g, k);
+          }
+        }
+        __syncwarp();
+        ++count;
+        if (++s == C::kSlots) {
+          s = 0;
+          ph ^= 1;
+        }
+      }
+    }
+    if (lane == 0) *issued = count;
+  } else if (warp == 1) {
+    // =========================== MMA issue ===========================
+    // Order per key tile: P.V of A, next scores of A, P.V of B, next scores of B, so
+    // that one query tile's products run under the other one's softmax.  The tensor
+    // pipe takes them in this order, so scores may follow the P.V that reads the
+    // weights they overwrite without a wait between the two.
+    if (T.n > 0) {
+      bool ok = mbar_wait_converged(bar(B_Q), 0, abort_flag, p.status, wait_ns);
+      int ks = 0, kph = 0, vs = 0, vph = 0;  // ring places of the K tile at hand and of the V tile
+      auto step = [&](int& s, int& ph, int by) {
+        s += by;
+        if (s >= C::kSlots) {
+          s -= C::kSlots;
+          ph ^= 1;
+        }
+      };
+      auto wait_full = [&](int s, int ph) { return mbar_wait_converged(full(s), ph, abort_flag, p.status, wait_ns); };
+      // scores of tile i over the K tile at (ks, kph)
+      auto scores = [&](int i) -> bool {
+        int s = ks, ph = kph;
+#pragma unroll
+        for (int c = 0; c < C::kQk; ++c) {
+          if (!wait_full(s, ph)) return false;
+          tc_fence_after();
+          const uint64_t dq = desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024);
+          const uint64_t dk = desc_sw128(sa + C::kRing + s * kChunk, 16, 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) mma_1_elect(tmem + 128u * i, dq + 2 * kk, dk + 2 * kk, kIdescS, (c | kk) != 0);
+          step(s, ph, 1);
+        }
+        commit_1_elect(bar(B_S + i));
+        return true;
+      };
+      auto release = [&](int s, int n) {
+        for (int c = 0; c < n; ++c) {
+          commit_1_elect(empty(s));
+          if (++s == C::kSlots) s = 0;
+        }
+      };
+      auto sees = [&](int i, int j) { return j >= T.from[i] && j < T.to[i]; };
+      for (int i = 0; ok && i < 2; ++i)
+        if (sees(i, 0)) ok = scores(i);
+      if (ok) release(ks, C::kQk);
+      for (int j = 0; ok && j < T.n; ++j) {
+        vs = ks;
+        vph = kph;
+        step(vs, vph, C::kQk);
+        step(ks, kph, C::kPer);
+        for (int i = 0; ok && i < 2; ++i) {
+          if (sees(i, j)) {
+            const int it = j - T.from[i];
+            int s = vs, ph = vph;
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && mbar_wait_converged(bar(B_P + 2 * i + half), it & 1, abort_flag, p.status, wait_ns) && wait_full(s, ph);
+              if (!ok) break;
+              tc_fence_after();
+              const uint64_t dv = desc_sw128(sa + C::kRing + s * kChunk, kChunk / 2, 1024);
+              // 16 keys a step: weights in 8 columns, V rows 16 kk
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_1_ts_elect(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half + 8u * kk, dv + ((kk * 2048) >> 4),
+                               kIdescPV, (it | half | kk) != 0);
+              step(s, ph, 1);
+            }
+            if (ok && j + 1 == T.to[i]) commit_1_elect(bar(B_O + i));
+          }
+          if (ok && i == 1) release(vs, 2);
+          if (ok && sees(i, j + 1)) ok = scores(i);
+          if (ok && i == 1 && j + 1 < T.n) release(ks, C::kQk);
+        }
+      }
+      commit_1_elect(bar(B_DRAIN));
+      int keep = 0;
+      mbar_wait_converged(bar(B_DRAIN), 0, &keep, p.status, kDrainNs);
+    }
+  } else if (warp >= 4) {
+    // ================ softmax: a thread per query row ================
+    const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t cs = 128u * t, co = kTmemO + 128u * t;
+    const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
+    float m_used = -CUDART_INF_F, l = 0.f;
+    for (int j = T.from[t]; j < T.to[t]; ++j) {
+      if (!mbar_wait_converged(bar(B_S + t), (j - T.from[t]) & 1, abort_flag, p.status, wait_ns)) break;
+      tc_fence_after();
+      uint32_t sr[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(tl + cs + 32u * c, sr[c]);
+      tmem_wait_ld();
+      const int kb = T.k0 + 128 * j;
+      const bool part = lo > kb || hi < kb + 128;
+      const bool masked = __any_sync(0xffffffffu, part);
+      if (masked) {
+        const uint32_t a = (uint32_t)max(lo - kb, 0), n = (uint32_t)max(min(hi - kb, 128) - (int)a, 0);
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if ((uint32_t)k - a >= n) sr[k >> 5][k & 31] = 0xff800000u;
+      }
+      float mx4[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) mx4[k] = __uint_as_float(sr[0][k]);
+#pragma unroll
+      for (int k = 4; k < 128; k += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int u = k + 2 * i, w = k + 2 * i + 1;
+          if (w < 128) mx4[i] = max3(mx4[i], __uint_as_float(sr[u >> 5][u & 31]), __uint_as_float(sr[w >> 5][w & 31]));
+        }
+      const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]) * p.scale_log2;
+      float alpha = 1.f;
+      bool resc = false;
+      if (mx > m_used + kRescale || m_used == -CUDART_INF_F) {
+        // (the first finite maximum: nothing to rescale, O holds zeros for this row)
+        if (mx > -CUDART_INF_F) {
+          alpha = ex2_approx(m_used - mx);
+          resc = l != 0.f;
+          l *= alpha;
+          m_used = mx;
+        }
+      }
+      // a NaN or an infinite maximum: the row is done over in fp32 at the end
+      if (!(mx < CUDART_INF_F)) l = CUDART_NAN_F;
+      const float nref = m_used == -CUDART_INF_F ? 0.f : -m_used;
+      if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tl + co + 32u * c, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+          tmem_st32(tl + co + 32u * c, o);
+        }
+        tmem_wait_st();
+      }
+      // weights 2^(s scale - m) over the scores, 64 keys at a time; in tiles without a
+      // mask a quarter of the exponentials go to the FMA pipe
+      const uint64_t nref2 = pack2(nref, nref);
+      uint64_t sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+      auto weights = [&](int half, bool poly) {
+        uint32_t pk[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int u = 64 * half + 2 * k;
+          const uint64_t x = fma2(pack2(__uint_as_float(sr[u >> 5][u & 31]), __uint_as_float(sr[u >> 5][(u & 31) + 1])),
+                                  scale2, nref2);
+          float p0, p1;
+          if (poly && (k & 3) == 3) {
+            exp2_poly2(x, p0, p1);
+          } else {
+            unpack2(x, p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+          }
+          sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
+          pk[k] = pack_bf16(p0, p1);
+        }
+        tmem_st32(tl + cs + 32u * half, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(bar(B_P + 2 * t + half));
+      };
+      const bool exact = masked || __any_sync(0xffffffffu, nref == 0.f);
+      if (exact) {
+        weights(0, false);
+        weights(1, false);
+      } else {
+        weights(0, true);
+        weights(1, true);
+      }
+      float s0, s1;
+      unpack2(add2(sum[0], sum[1]), s0, s1);
+      l += s0 + s1;
+    }
+    // ---- o = O / l, lse
+    const bool any = T.to[t] > T.from[t];
+    if (any) {
+      mbar_wait_converged(bar(B_O + t), 0, abort_flag, p.status, wait_ns);
+      tc_fence_after();
+    }
+    const bool live = any && __shfl_sync(0xffffffffu, *abort_flag, 0) == 0;
+    const bool mine = hi > lo;
+    const float inv = l == 0.f || !live ? 0.f : 1.f / l;
+    const int64_t orow = (int64_t)qi * p.H + h;
+    bool odd = live && mine && !(fabsf(l) < CUDART_INF_F);
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t o[32];
+      if (live) {
+        tmem_ld32(tl + co + 32u * c, o);
+        tmem_wait_ld();
+      } else {
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = 0u;
+      }
+      float bad = 0.f;  // a NaN once any value is infinite or not a number
+#pragma unroll
+      for (int k = 0; k < 32; ++k) bad = fmaf(__uint_as_float(o[k]), 0.f, bad);
+      odd = odd || (live && mine && bad != 0.f);
+      if (mine) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kDv + 32 * c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          dst[k] = make_uint4(pack_bf16(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
+                              pack_bf16(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
+                              pack_bf16(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
+                              pack_bf16(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
+      }
+    }
+    if (mine && p.lse) p.lse[orow] = inv == 0.f ? -CUDART_INF_F : (m_used + log2f(l)) * 0.6931471805599453f;
+    // An infinite or NaN value that a row does not see has met its zero weight in the
+    // product with V (0 x inf): such rows, and those that see one, are done over from
+    // the definition.
+    __syncwarp();
+    for (uint32_t again = __ballot_sync(0xffffffffu, odd); again; again &= again - 1) {
+      const int r = __ffs(again) - 1;
+      attend_row<PE>(p, __shfl_sync(0xffffffffu, qi, r), h, __shfl_sync(0xffffffffu, lo, r), __shfl_sync(0xffffffffu, hi, r),
+                     lane);
+    }
+    tc_fence_before();
+  }
+
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    // no load may outlive the block: the queries of a block without keys, and after a
+    // wait that ran out the last round of the ring (all waits bounded)
+    int give_up = 0;
+    mbar_wait(bar(B_Q), 0, &give_up, nullptr, kDrainNs);
+    for (int i = *abort_flag ? max(0, *issued - C::kSlots) : *issued; i < *issued; ++i)
+      mbar_wait(full(i % C::kSlots), (i / C::kSlots) & 1, &give_up, nullptr, kDrainNs);
+  }
+  __syncthreads();
+  if (warp == 1) tmem_dealloc_1(tmem, 512);
+}
+
+template <bool PE>
+cudaError_t launch_tiles(const mla_prefill_packed_args_t* a, const PackedParams& p, cudaStream_t stream) {
+  using C = Cfg<PE>;
+  // a dimension of one may come with any stride: the map needs a valid one
+  auto bytes = [](int64_t stride, int64_t extent) { return (uint64_t)(extent > 1 ? 2 * stride : 256); };
+  const uint64_t n = a->n_tok;
+  CUtensorMap qn, qp = {}, kn, kp = {}, v;
+  if (!tma_map_3d_fresh(&qn, a->q_nope, kDn, a->H, n, bytes(a->q_nope_head, a->H), bytes(a->q_nope_tok, n), 64, 1, 128) ||
+      !tma_map_3d_fresh(&kn, a->k_nope, kDn, a->H_kv, n, bytes(a->k_nope_head, a->H_kv), bytes(a->k_nope_tok, n), 64, 1, 128) ||
+      !tma_map_3d_fresh(&v, a->v, kDv, a->H_kv, n, bytes(a->v_head, a->H_kv), bytes(a->v_tok, n), 64, 1, 64))
+    return cudaErrorInvalidValue;
+  if (PE && (!tma_map_3d_fresh(&qp, a->q_pe, kDr, a->H, n, bytes(a->q_pe_head, a->H), bytes(a->q_pe_tok, n), 64, 1, 128) ||
+             !tma_map_3d_fresh(&kp, a->k_pe, kDr, 1, n, 256, bytes(a->k_pe_tok, n), 64, 1, 128)))
+    return cudaErrorInvalidValue;
+  static PerDeviceOnce attrs;
+  const cudaError_t e = once_per_device(attrs, [&]() {
+    return cudaFuncSetAttribute(packed_attn_kernel<PE>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_pdl(packed_attn_kernel<PE>, dim3((unsigned)((int64_t)p.blocks * a->H)), dim3(kThreads), C::kSmem, stream, qn,
+                    qp, kn, kp, v, p);
 }
 
 }  // namespace
@@ -129,9 +597,9 @@ cudaError_t launch_prefill_packed(const mla_prefill_packed_args_t* a, cudaStream
   p.share = a->H / a->H_kv;
   p.causal = a->causal;
   p.scale_log2 = a->softmax_scale * kLog2e;
-  const dim3 grid((unsigned)(((int64_t)a->n_tok * a->H + 3) / 4));
-  return a->d_r ? launch_pdl(packed_rows_kernel<true>, grid, dim3(128), 0, stream, p)
-                : launch_pdl(packed_rows_kernel<false>, grid, dim3(128), 0, stream, p);
+  p.blocks = (int)(((int64_t)a->n_tok + kRows - 1) / kRows);
+  p.wait_ns = device_wait_limit_ns();
+  return a->d_r ? launch_tiles<true>(a, p, stream) : launch_tiles<false>(a, p, stream);
 }
 
 }  // namespace mla

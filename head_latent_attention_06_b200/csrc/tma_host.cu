@@ -45,15 +45,7 @@ MapKey g_keys[kCache];
 CUtensorMap g_maps[kCache];
 int g_count = 0, g_next = 0;
 
-bool encode(CUtensorMap* m, const MapKey& k) {
-  {
-    std::lock_guard<std::mutex> lock(g_mu);
-    for (int i = 0; i < g_count; ++i)
-      if (g_keys[i] == k) {
-        *m = g_maps[i];
-        return true;
-      }
-  }
+bool encode_fresh(CUtensorMap* m, const MapKey& k) {
   auto enc = get_encode();
   if (!enc) return false;
   cuuint64_t dims[5], strides[4];
@@ -67,7 +59,19 @@ bool encode(CUtensorMap* m, const MapKey& k) {
   CUresult res = enc(m, k.dtype, k.rank, const_cast<void*>(k.ptr), dims, strides,
                      box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, k.swizzle,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (res != CUDA_SUCCESS) return false;
+  return res == CUDA_SUCCESS;
+}
+
+bool encode(CUtensorMap* m, const MapKey& k) {
+  {
+    std::lock_guard<std::mutex> lock(g_mu);
+    for (int i = 0; i < g_count; ++i)
+      if (g_keys[i] == k) {
+        *m = g_maps[i];
+        return true;
+      }
+  }
+  if (!encode_fresh(m, k)) return false;
   std::lock_guard<std::mutex> lock(g_mu);
   const int slot = g_count < kCache ? g_count++ : (g_next++ % kCache);
   g_keys[slot] = k;
@@ -89,6 +93,13 @@ bool tma_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint6
   MapKey k{ptr, 3, {d0, d1, d2, 1, 1}, {s1, s2, 0, 0}, {b0, b1, b2, 1, 1},
            CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B};
   return encode(m, k);
+}
+
+bool tma_map_3d_fresh(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
+                      uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2) {
+  MapKey k{ptr, 3, {d0, d1, d2, 1, 1}, {s1, s2, 0, 0}, {b0, b1, b2, 1, 1},
+           CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B};
+  return encode_fresh(m, k);
 }
 
 bool tma_map_nd(CUtensorMap* m, const void* ptr, uint32_t rank, const uint64_t* dims, const uint64_t* strides,
