@@ -107,6 +107,12 @@ struct Cfg {
   static constexpr int kQk = PE ? 3 : 2;              // 64-value chunks of a query or key
   static constexpr int kSlots = PE ? 8 : 10;          // ring of K and V chunks
   static constexpr int kPer = kQk + 2;                // chunks of one key tile: K, then V in halves of 64 keys
+  // K(j) may go in once the item kWaitK before it has been read, V(j) once the item
+  // kWaitV before it has: with 8 slots of which a key tile takes 3 + 2, K(j) ends at 5 j + 3
+  // and needs V(j - 2), which ends at 5 j - 5, gone; V(j) ends at 5 j + 5 and needs
+  // K(j - 1), which ends at 5 j - 2, gone.  With 10 slots of 2 + 2, K(j) needs 4 j - 8
+  // (V(j - 3)) and V(j) 4 j - 6 (K(j - 2)).
+  static constexpr int kWaitK = PE ? 3 : 5, kWaitV = PE ? 3 : 5;
   static constexpr uint32_t kRing = 2 * kQk * kChunk;
   static constexpr uint32_t kBars = kRing + kSlots * kChunk;
   static constexpr uint32_t kSmem = kBars + 512 + 1024;
@@ -119,7 +125,7 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
 constexpr float kRescale = 8.0f;
 // barriers; [2] per tile, P[2 t + half]
-constexpr int B_Q = 0, B_S = 1, B_P = 3, B_O = 7, B_DRAIN = 9, B_FULL = 10;
+constexpr int B_Q = 0, B_S = 1, B_P = 3, B_O = 7, B_DRAIN = 9, B_FULL = 10, B_EMPTY = 18, B_COUNT = 26;
 
 struct Tiles {
   int k0;         // first key of the block's first key tile
@@ -164,6 +170,10 @@ MLA_DEVI void exp2_poly2(uint64_t x, float& p0, float& p1) {
   p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
   p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
+template <bool kOn>
+struct Poly {
+  static constexpr bool value = kOn;
+};
 // maximum of three that keeps a NaN
 MLA_DEVI float max3(float a, float b, float c) {
   float r;
@@ -181,11 +191,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sa = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (sa - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // warp-uniform, and known to be: what the MMA warp computes stays in uniform registers
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sa + C::kBars + 8u * i; };
-  auto full = [&](int s) -> uint32_t { return bar(B_FULL + s); };
-  auto empty = [&](int s) -> uint32_t { return bar(B_FULL + C::kSlots + s); };
-  int* words = reinterpret_cast<int*>(sm + C::kBars + 8 * (B_FULL + 2 * C::kSlots));
+  auto full = [&](int item) -> uint32_t { return bar(B_FULL + (item & 7)); };
+  auto empty = [&](int item) -> uint32_t { return bar(B_EMPTY + (item & 7)); };
+  auto slot = [&](int s) -> uint32_t { return sa + C::kRing + (s % C::kSlots) * kChunk; };
+  int* words = reinterpret_cast<int*>(sm + C::kBars + 8 * B_COUNT);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   volatile int* abort_flag = words + 1;
   int* issued = words + 2;
@@ -212,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_O + t), 1);
     }
     mbar_init(bar(B_DRAIN), 1);
-    for (int s = 0; s < C::kSlots; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(full(i), 1);
+      mbar_init(empty(i), 1);
     }
     fence_mbar_init();
   }
@@ -277,36 +289,41 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
 
+  // 384 threads launched with 168 registers: 128 x 80 + 256 x 208 is within that
+  if (warp < 4) {
+    regs_dec<80>();
   if (warp == 0) {
     // =========================== loads ===========================
-    // K chunks of a tile, then its V in halves of 64 keys, round the ring
-    int s = 0, ph = 1, count = 0;
+    // Items in the ring, each with a full and an empty barrier of eight taken in turn:
+    // K(j) is item 2 j (kQk slots from kPer j on), V(j) item 2 j + 1 (two slots after
+    // it).  An item goes into slots whose last holders have been read: see Cfg::kWaitK.
+    int count = 0;
     bool ok = true;
     for (int j = 0; ok && j < T.n; ++j) {
       const int key = T.k0 + 128 * j;
 #pragma unroll
-      for (int c = 0; c < C::kPer; ++c) {
-        ok = ok && mbar_wait_converged(empty(s), ph, abort_flag, p.status, wait_ns);
+      for (int v = 0; v < 2; ++v) {
+        const int item = 2 * j + v, last = item - (v ? C::kWaitV : C::kWaitK);
+        if (last >= 0) ok = ok && mbar_wait_converged(empty(last), (last >> 3) & 1, abort_flag, p.status, wait_ns);
         if (!ok) break;
         if (lane == 0) {
-          const uint32_t dst = sa + C::kRing + s * kChunk;
-          mbar_arrive_expect_tx_local(full(s), kChunk);
-          if (c < 2) {
-            tma_load_3d_cta(dst, &tm_kn, full(s), 64 * c, g, key);
-          } else if (PE && c == 2) {
-            tma_load_3d_cta(dst, &tm_kp, full(s), 0, 0, key);
+          const uint32_t f = full(item);
+          const int s = C::kPer * j + (v ? C::kQk : 0);
+          mbar_arrive_expect_tx_local(f, (v ? 2 : C::kQk) * kChunk);
+          if (v == 0) {
+            tma_load_3d_cta(slot(s), &tm_kn, f, 0, g, key);
+            tma_load_3d_cta(slot(s + 1), &tm_kn, f, 64, g, key);
+            if constexpr (PE) tma_load_3d_cta(slot(s + 2), &tm_kp, f, 0, 0, key);
           } else {
-            const int k = key + 64 * (c - C::kQk);
-            tma_load_3d_cta(dst, &tm_v, full(s), 0, g, k);
-            tma_load_3d_cta(dst + kChunk / 2, &tm_v, full(s), 64, g, k);
+            // halves of 64 keys, 128 values each
+            for (int half = 0; half < 2; ++half) {
+              tma_load_3d_cta(slot(s + half), &tm_v, f, 0, g, key + 64 * half);
+              tma_load_3d_cta(slot(s + half) + kChunk / 2, &tm_v, f, 64, g, key + 64 * half);
+            }
           }
         }
         __syncwarp();
-        ++count;
-        if (++s == C::kSlots) {
-          s = 0;
-          ph ^= 1;
-        }
+        count = item + 1;
       }
     }
     if (lane == 0) *issued = count;
@@ -318,75 +335,60 @@ __global__ void __launch_bounds__(kThreads, 1)
     // weights they overwrite without a wait between the two.
     if (T.n > 0) {
       bool ok = mbar_wait_converged(bar(B_Q), 0, abort_flag, p.status, wait_ns);
-      int ks = 0, kph = 0, vs = 0, vph = 0;  // ring places of the K tile at hand and of the V tile
-      auto step = [&](int& s, int& ph, int by) {
-        s += by;
-        if (s >= C::kSlots) {
-          s -= C::kSlots;
-          ph ^= 1;
-        }
+      auto arrived = [&](int item) {
+        const bool in = mbar_wait_converged(full(item), (item >> 3) & 1, abort_flag, p.status, wait_ns);
+        tc_fence_after();
+        return in;
       };
-      auto wait_full = [&](int s, int ph) { return mbar_wait_converged(full(s), ph, abort_flag, p.status, wait_ns); };
-      // scores of tile i over the K tile at (ks, kph)
-      auto scores = [&](int i) -> bool {
-        int s = ks, ph = kph;
+      // scores of query tile i over K(j)
+      auto scores = [&](int i, int j) {
 #pragma unroll
-        for (int c = 0; c < C::kQk; ++c) {
-          if (!wait_full(s, ph)) return false;
-          tc_fence_after();
-          const uint64_t dq = desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024);
-          const uint64_t dk = desc_sw128(sa + C::kRing + s * kChunk, 16, 1024);
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) mma_1_elect(tmem + 128u * i, dq + 2 * kk, dk + 2 * kk, kIdescS, (c | kk) != 0);
-          step(s, ph, 1);
-        }
+        for (int c = 0; c < C::kQk; ++c)
+          mma_1_x4_elect<2, 2>(tmem + 128u * i, desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024),
+                               desc_sw128(slot(C::kPer * j + c), 16, 1024), kIdescS, c != 0);
         commit_1_elect(bar(B_S + i));
-        return true;
-      };
-      auto release = [&](int s, int n) {
-        for (int c = 0; c < n; ++c) {
-          commit_1_elect(empty(s));
-          if (++s == C::kSlots) s = 0;
-        }
       };
       auto sees = [&](int i, int j) { return j >= T.from[i] && j < T.to[i]; };
+      ok = ok && arrived(0);
       for (int i = 0; ok && i < 2; ++i)
-        if (sees(i, 0)) ok = scores(i);
-      if (ok) release(ks, C::kQk);
+        if (sees(i, 0)) scores(i, 0);
+      if (ok) commit_1_elect(empty(0));
       for (int j = 0; ok && j < T.n; ++j) {
-        vs = ks;
-        vph = kph;
-        step(vs, vph, C::kQk);
-        step(ks, kph, C::kPer);
+        bool in_v = false, in_k = false;  // V(j), K(j + 1) have been waited for
         for (int i = 0; ok && i < 2; ++i) {
           if (sees(i, j)) {
             const int it = j - T.from[i];
-            int s = vs, ph = vph;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              ok = ok && mbar_wait_converged(bar(B_P + 2 * i + half), it & 1, abort_flag, p.status, wait_ns) && wait_full(s, ph);
+              ok = ok && mbar_wait_converged(bar(B_P + 2 * i + half), it & 1, abort_flag, p.status, wait_ns);
+              if (ok && !in_v) in_v = ok = arrived(2 * j + 1);
               if (!ok) break;
               tc_fence_after();
-              const uint64_t dv = desc_sw128(sa + C::kRing + s * kChunk, kChunk / 2, 1024);
-              // 16 keys a step: weights in 8 columns, V rows 16 kk
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_1_ts_elect(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half + 8u * kk, dv + ((kk * 2048) >> 4),
-                               kIdescPV, (it | half | kk) != 0);
-              step(s, ph, 1);
+              // 16 keys a step: weights in 8 columns, V rows 2 KB further on
+              mma_1_ts_x4_elect<8, 128>(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half,
+                                        desc_sw128(slot(C::kPer * j + C::kQk + half), kChunk / 2, 1024), kIdescPV,
+                                        (it | half) != 0);
             }
             if (ok && j + 1 == T.to[i]) commit_1_elect(bar(B_O + i));
           }
-          if (ok && i == 1) release(vs, 2);
-          if (ok && sees(i, j + 1)) ok = scores(i);
-          if (ok && i == 1 && j + 1 < T.n) release(ks, C::kQk);
+          if (ok && i == 1) {
+            if (!in_v) ok = arrived(2 * j + 1);
+            commit_1_elect(empty(2 * j + 1));
+          }
+          if (ok && j + 1 < T.n) {
+            if (!in_k && (sees(i, j + 1) || i == 1)) in_k = ok = arrived(2 * j + 2);
+            if (ok && sees(i, j + 1)) scores(i, j + 1);
+            if (ok && i == 1) commit_1_elect(empty(2 * j + 2));
+          }
         }
       }
       commit_1_elect(bar(B_DRAIN));
       int keep = 0;
       mbar_wait_converged(bar(B_DRAIN), 0, &keep, p.status, kDrainNs);
     }
-  } else if (warp >= 4) {
+  }
+  } else {
+    regs_inc<208>();
     // ================ softmax: a thread per query row ================
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t cs = 128u * t, co = kTmemO + 128u * t;
@@ -400,64 +402,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) tmem_ld32(tl + cs + 32u * c, sr[c]);
       tmem_wait_ld();
       const int kb = T.k0 + 128 * j;
-      const bool part = lo > kb || hi < kb + 128;
-      const bool masked = __any_sync(0xffffffffu, part);
-      if (masked) {
-        const uint32_t a = (uint32_t)max(lo - kb, 0), n = (uint32_t)max(min(hi - kb, 128) - (int)a, 0);
+      auto score = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
+      // four running maxima, joined
+      auto maximum = [&]() {
+        float m4[4];
 #pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if ((uint32_t)k - a >= n) sr[k >> 5][k & 31] = 0xff800000u;
-      }
-      float mx4[4];
+        for (int k = 0; k < 4; ++k) m4[k] = score(k);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) mx4[k] = __uint_as_float(sr[0][k]);
+        for (int k = 4; k < 124; k += 8)
 #pragma unroll
-      for (int k = 4; k < 128; k += 8)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int u = k + 2 * i, w = k + 2 * i + 1;
-          if (w < 128) mx4[i] = max3(mx4[i], __uint_as_float(sr[u >> 5][u & 31]), __uint_as_float(sr[w >> 5][w & 31]));
-        }
-      const float mx = max3(max3(mx4[0], mx4[1], mx4[2]), mx4[3], mx4[3]) * p.scale_log2;
-      float alpha = 1.f;
-      bool resc = false;
-      if (mx > m_used + kRescale || m_used == -CUDART_INF_F) {
-        // (the first finite maximum: nothing to rescale, O holds zeros for this row)
-        if (mx > -CUDART_INF_F) {
-          alpha = ex2_approx(m_used - mx);
-          resc = l != 0.f;
-          l *= alpha;
-          m_used = mx;
-        }
-      }
-      // a NaN or an infinite maximum: the row is done over in fp32 at the end
-      if (!(mx < CUDART_INF_F)) l = CUDART_NAN_F;
-      const float nref = m_used == -CUDART_INF_F ? 0.f : -m_used;
-      if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32(tl + co + 32u * c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-          tmem_st32(tl + co + 32u * c, o);
-        }
-        tmem_wait_st();
-      }
-      // weights 2^(s scale - m) over the scores, 64 keys at a time; in tiles without a
-      // mask a quarter of the exponentials go to the FMA pipe
-      const uint64_t nref2 = pack2(nref, nref);
-      uint64_t sum[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
-      auto weights = [&](int half, bool poly) {
-        uint32_t pk[32];
+          for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], score(k + 2 * i), score(k + 2 * i + 1));
+        m4[0] = max3(m4[0], score(124), score(125));
+        m4[1] = max3(m4[1], score(126), score(127));
+        return max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]) * p.scale_log2;
+      };
+      // weights 2^(s scale - m) of 64 keys, in bf16 pairs; with `kPoly` a part of the
+      // exponentials goes to the FMA pipe
+      uint64_t sum[2] = {0, 0};
+      auto weights = [&](int half, float ref, auto poly, uint32_t (&pk)[32]) {
+        const uint64_t ref2 = pack2(ref, ref);
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           const int u = 64 * half + 2 * k;
-          const uint64_t x = fma2(pack2(__uint_as_float(sr[u >> 5][u & 31]), __uint_as_float(sr[u >> 5][(u & 31) + 1])),
-                                  scale2, nref2);
+          const uint64_t x = fma2(pack2(score(u), score(u + 1)), scale2, ref2);
           float p0, p1;
-          if (poly && (k & 3) == 3) {
+          if (decltype(poly)::value && (k & 3) == 3) {
             exp2_poly2(x, p0, p1);
           } else {
             unpack2(x, p0, p1);
@@ -467,19 +436,69 @@ __global__ void __launch_bounds__(kThreads, 1)
           sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
           pk[k] = pack_bf16(p0, p1);
         }
+      };
+      // over the scores, and to the MMA warp
+      auto hand_over = [&](int half, uint32_t (&pk)[32]) {
         tmem_st32(tl + cs + 32u * half, pk);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_local(bar(B_P + 2 * t + half));
       };
-      const bool exact = masked || __any_sync(0xffffffffu, nref == 0.f);
-      if (exact) {
-        weights(0, false);
-        weights(1, false);
-      } else {
-        weights(0, true);
-        weights(1, true);
+      const bool masked = __any_sync(0xffffffffu, lo > kb || hi < kb + 128);
+      bool careful = masked || __any_sync(0xffffffffu, m_used == -CUDART_INF_F);
+      if (!careful) {
+        // Most tiles raise no maximum by more than 2^8: the weights of the first half
+        // are formed against the old one while the new one is found.
+        uint32_t pk[32];
+        weights(0, -m_used, Poly<true>(), pk);
+        const float mx = maximum();
+        careful = __any_sync(0xffffffffu, !(mx <= m_used + kRescale));
+        if (!careful) {
+          hand_over(0, pk);
+          weights(1, -m_used, Poly<true>(), pk);
+          hand_over(1, pk);
+        } else {
+          sum[0] = sum[1] = 0;
+        }
+      }
+      if (careful) {
+        if (masked) {
+          const uint32_t a = (uint32_t)max(lo - kb, 0), n = (uint32_t)max(min(hi - kb, 128) - (int)a, 0);
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if ((uint32_t)k - a >= n) sr[k >> 5][k & 31] = 0xff800000u;
+        }
+        const float mx = maximum();
+        float alpha = 1.f;
+        bool resc = false;
+        if (mx > m_used + kRescale) {
+          // (with no weight so far there is nothing to rescale: O holds zeros for this row)
+          alpha = ex2_approx(m_used - mx);
+          resc = l != 0.f;
+          l *= alpha;
+          m_used = mx;
+        }
+        // a NaN or an infinite maximum: the row is done over in fp32 at the end
+        if (!(mx < CUDART_INF_F)) l = CUDART_NAN_F;
+        if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tl + co + 32u * c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            tmem_st32(tl + co + 32u * c, o);
+          }
+          tmem_wait_st();
+        }
+        const float ref = m_used == -CUDART_INF_F ? 0.f : -m_used;
+        uint32_t pk[32];
+        weights(0, ref, Poly<false>(), pk);
+        hand_over(0, pk);
+        weights(1, ref, Poly<false>(), pk);
+        hand_over(1, pk);
       }
       float s0, s1;
       unpack2(add2(sum[0], sum[1]), s0, s1);
@@ -539,8 +558,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // wait that ran out the last round of the ring (all waits bounded)
     int give_up = 0;
     mbar_wait(bar(B_Q), 0, &give_up, nullptr, kDrainNs);
-    for (int i = *abort_flag ? max(0, *issued - C::kSlots) : *issued; i < *issued; ++i)
-      mbar_wait(full(i % C::kSlots), (i / C::kSlots) & 1, &give_up, nullptr, kDrainNs);
+    for (int i = *abort_flag ? max(0, *issued - 8) : *issued; i < *issued; ++i)
+      mbar_wait(full(i), (i >> 3) & 1, &give_up, nullptr, kDrainNs);
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc_1(tmem, 512);
