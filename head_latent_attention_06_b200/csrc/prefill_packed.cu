@@ -97,7 +97,7 @@ MLA_DEVI void attend_row(const PackedParams& p, int t, int h, int lo, int hi, in
 }
 
 // ---------------------------------------------------------------- tiles
-constexpr int kThreads = 384;               // warp 0 loads, warp 1 MMA, warps 4..7 tile A, 8..11 tile B
+constexpr int kThreads = 384;               // warp 0 loads, warps 1 and 2 MMA, warps 4..7 tile A, 8..11 tile B
 constexpr int kRows = 256;                  // packed rows of a CTA: tile A the first 128, B the others
 constexpr uint32_t kChunk = 128 * 128;      // 16 KB: 128 rows x 64 values, or 64 keys x 128 values
 constexpr int kHeadGroup = 8;               // heads whose blocks run side by side
@@ -125,7 +125,7 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
 constexpr float kRescale = 8.0f;
 // barriers; [2] per tile, P[2 t + half]
-constexpr int B_Q = 0, B_S = 1, B_P = 3, B_O = 7, B_DRAIN = 9, B_FULL = 10, B_EMPTY = 18, B_COUNT = 26;
+constexpr int B_Q = 0, B_S = 1, B_P = 3, B_O = 7, B_DRAIN = 9, B_FULL = 11, B_EMPTY = 19, B_TURN = 27, B_COUNT = 29;
 
 struct Tiles {
   int k0;         // first key of the block's first key tile
@@ -222,11 +222,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(B_P + 2 * t), 4);
       mbar_init(bar(B_P + 2 * t + 1), 4);
       mbar_init(bar(B_O + t), 1);
+      mbar_init(bar(B_DRAIN + t), 1);
+      mbar_init(bar(B_TURN + t), 1);
     }
-    mbar_init(bar(B_DRAIN), 1);
     for (int i = 0; i < 8; ++i) {
       mbar_init(full(i), 1);
-      mbar_init(empty(i), 1);
+      mbar_init(empty(i), 2);  // both query tiles have read it
     }
     fence_mbar_init();
   }
@@ -292,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // 384 threads launched with 168 registers: 128 x 80 + 256 x 208 is within that
   if (warp < 4) {
     regs_dec<80>();
-  if (warp == 0) {
+    if (warp == 0) {
     // =========================== loads ===========================
     // Items in the ring, each with a full and an empty barrier of eight taken in turn:
     // K(j) is item 2 j (kQk slots from kPer j on), V(j) item 2 j + 1 (two slots after
@@ -327,64 +328,69 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (lane == 0) *issued = count;
-  } else if (warp == 1) {
+  } else if (warp < 3) {
     // =========================== MMA issue ===========================
-    // Order per key tile: P.V of A, next scores of A, P.V of B, next scores of B, so
-    // that one query tile's products run under the other one's softmax.  The tensor
-    // pipe takes them in this order, so scores may follow the P.V that reads the
-    // weights they overwrite without a wait between the two.
+    // One warp per query tile: P.V, then the next scores, while the other tile's
+    // softmax runs under them.  (One warp for both issued 40 MMAs, six waits and four
+    // commits per key tile, 3500 cycles of it, more than the 2560 that the tensor pipe
+    // needs.)  The pipe takes a warp's products in order, so scores may follow the P.V
+    // that reads the weights they overwrite without a wait between the two.
+    const int i = warp - 1;
     if (T.n > 0) {
       bool ok = mbar_wait_converged(bar(B_Q), 0, abort_flag, p.status, wait_ns);
       auto arrived = [&](int item) {
-        const bool in = mbar_wait_converged(full(item), (item >> 3) & 1, abort_flag, p.status, wait_ns);
-        tc_fence_after();
-        return in;
+        return mbar_wait_converged(full(item), (item >> 3) & 1, abort_flag, p.status, wait_ns);
       };
-      // scores of query tile i over K(j)
-      auto scores = [&](int i, int j) {
-#pragma unroll
-        for (int c = 0; c < C::kQk; ++c)
-          mma_1_x4_elect<2, 2>(tmem + 128u * i, desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024),
-                               desc_sw128(slot(C::kPer * j + c), 16, 1024), kIdescS, c != 0);
-        commit_1_elect(bar(B_S + i));
+      auto pass_turn = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(bar(B_TURN + 1 - i));
+        __syncwarp();
       };
-      auto sees = [&](int i, int j) { return j >= T.from[i] && j < T.to[i]; };
-      ok = ok && arrived(0);
-      for (int i = 0; ok && i < 2; ++i)
-        if (sees(i, 0)) scores(i, 0);
-      if (ok) commit_1_elect(empty(0));
-      for (int j = 0; ok && j < T.n; ++j) {
-        bool in_v = false, in_k = false;  // V(j), K(j + 1) have been waited for
-        for (int i = 0; ok && i < 2; ++i) {
-          if (sees(i, j)) {
-            const int it = j - T.from[i];
+      auto sees = [&](int j) { return j >= T.from[i] && j < T.to[i]; };
+      // scores over K(j), which then has been read by this tile
+      auto scores = [&](int j) {
+        if (!arrived(2 * j)) return false;
+        if (j > 0) pass_turn();
+        if (sees(j)) {
+          tc_fence_after();
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              ok = ok && mbar_wait_converged(bar(B_P + 2 * i + half), it & 1, abort_flag, p.status, wait_ns);
-              if (ok && !in_v) in_v = ok = arrived(2 * j + 1);
-              if (!ok) break;
-              tc_fence_after();
-              // 16 keys a step: weights in 8 columns, V rows 2 KB further on
-              mma_1_ts_x4_elect<8, 128>(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half,
-                                        desc_sw128(slot(C::kPer * j + C::kQk + half), kChunk / 2, 1024), kIdescPV,
-                                        (it | half) != 0);
-            }
-            if (ok && j + 1 == T.to[i]) commit_1_elect(bar(B_O + i));
-          }
-          if (ok && i == 1) {
-            if (!in_v) ok = arrived(2 * j + 1);
-            commit_1_elect(empty(2 * j + 1));
-          }
-          if (ok && j + 1 < T.n) {
-            if (!in_k && (sees(i, j + 1) || i == 1)) in_k = ok = arrived(2 * j + 2);
-            if (ok && sees(i, j + 1)) scores(i, j + 1);
-            if (ok && i == 1) commit_1_elect(empty(2 * j + 2));
-          }
+          for (int c = 0; c < C::kQk; ++c)
+            mma_1_x4_elect<2, 2>(tmem + 128u * i, desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024),
+                                 desc_sw128(slot(C::kPer * j + c), 16, 1024), kIdescS, c != 0);
+          commit_1_elect(bar(B_S + i));
         }
+        commit_1_elect(empty(2 * j));
+        return true;
+      };
+      ok = ok && scores(0);
+      for (int j = 0; ok && j < T.n; ++j) {
+        // in turn: A's products of key tile j, then B's, then A's of the next
+        if (i + j > 0) ok = mbar_wait_converged(bar(B_TURN + i), (i ? j : j - 1) & 1, abort_flag, p.status, wait_ns);
+        ok = ok && arrived(2 * j + 1);
+        if (ok && sees(j)) {
+          const int it = j - T.from[i];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && mbar_wait_converged(bar(B_P + 2 * i + half), it & 1, abort_flag, p.status, wait_ns);
+            if (!ok) break;
+            tc_fence_after();
+            // 16 keys a step: weights in 8 columns, V rows 2 KB further on
+            mma_1_ts_x4_elect<8, 128>(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half,
+                                      desc_sw128(slot(C::kPer * j + C::kQk + half), kChunk / 2, 1024), kIdescPV,
+                                      (it | half) != 0);
+          }
+          if (ok && j + 1 == T.to[i]) commit_1_elect(bar(B_O + i));
+        }
+        if (!ok) break;
+        commit_1_elect(empty(2 * j + 1));
+        if (j + 1 < T.n)
+          ok = scores(j + 1);
+        else
+          pass_turn();
       }
-      commit_1_elect(bar(B_DRAIN));
+      commit_1_elect(bar(B_DRAIN + i));
       int keep = 0;
-      mbar_wait_converged(bar(B_DRAIN), 0, &keep, p.status, kDrainNs);
+      mbar_wait_converged(bar(B_DRAIN + i), 0, &keep, p.status, kDrainNs);
     }
   }
   } else {
