@@ -123,7 +123,9 @@ static_assert(Cfg<true>::kSmem <= 232448 && Cfg<false>::kSmem <= 232448, "shared
 constexpr uint32_t kTmemO = 256;
 constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
-constexpr float kRescale = 8.0f;
+constexpr float kRescale = 256.f;             // a tile's weights beyond this ask for a new reference
+constexpr float kBeyond = 1.152921504606847e18f;  // 2^60: no range is left to wait for it
+constexpr int kPolyPairs = 0x00;              // of eight pairs of exponentials, those on the FMA pipe
 // barriers; [2] per tile, P[2 t + half]
 constexpr int B_Q = 0, B_S = 1, B_P = 3, B_O = 7, B_DRAIN = 9, B_FULL = 11, B_EMPTY = 19, B_TURN = 27, B_COUNT = 29;
 
@@ -158,7 +160,7 @@ MLA_DEVI void exp2_poly2(uint64_t x, float& p0, float& p1) {
   x = pack2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
   const float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves round(x) in the low mantissa bits
   const uint64_t t = add2(x, pack2(kMagic, kMagic));
-  const uint64_t f = add2(x, add2(pack2(kMagic, kMagic), t ^ 0x8000000080000000ull));  // x - (t - magic)
+  const uint64_t f = fma2(add2(t, pack2(-kMagic, -kMagic)), pack2(-1.f, -1.f), x);
   uint64_t r = pack2(0.009570102207362652f, 0.009570102207362652f);
   r = fma2(r, f, pack2(0.05591785907745361f, 0.05591785907745361f));
   r = fma2(r, f, pack2(0.240247443318367f, 0.240247443318367f));
@@ -338,55 +340,50 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = warp - 1;
     if (T.n > 0) {
       bool ok = mbar_wait_converged(bar(B_Q), 0, abort_flag, p.status, wait_ns);
-      auto arrived = [&](int item) {
-        return mbar_wait_converged(full(item), (item >> 3) & 1, abort_flag, p.status, wait_ns);
+      auto wait = [&](int b, int parity) { return mbar_wait_converged(bar(b), parity & 1, abort_flag, p.status, wait_ns); };
+      auto arrived = [&](int item) { return wait(B_FULL + (item & 7), item >> 3); };
+      auto sees = [&](int j) { return j >= T.from[i] && j < T.to[i]; };
+      // scores over K(j)
+      auto scores = [&](int j) {
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < C::kQk; ++c)
+          mma_1_x4_elect<2, 2>(tmem + 128u * i, desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024),
+                               desc_sw128(slot(C::kPer * j + c), 16, 1024), kIdescS, c != 0);
+        commit_1_elect(bar(B_S + i));
       };
-      auto pass_turn = [&]() {
+      // the weights of half a key tile times V(j): 16 keys a step, weights in 8 columns, V
+      // rows 2 KB further on
+      auto values = [&](int j, int half) {
+        tc_fence_after();
+        mma_1_ts_x4_elect<8, 128>(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half,
+                                  desc_sw128(slot(C::kPer * j + C::kQk + half), kChunk / 2, 1024), kIdescPV,
+                                  (j > T.from[i] || half) ? 1u : 0u);
+      };
+      ok = ok && arrived(0);
+      if (ok) {
+        if (sees(0)) scores(0);
+        commit_1_elect(empty(0));
+      }
+      for (int j = 0; ok && j < T.n; ++j) {
+        const bool mine = sees(j), more = j + 1 < T.n;
+        ok = arrived(2 * j + 1);
+        if (mine) ok = ok && wait(B_P + 2 * i, j - T.from[i]);
+        // in turn: A's products of key tile j, then B's, then A's of the next
+        if (i + j > 0) ok = ok && wait(B_TURN + i, i ? j : j - 1);
+        if (!ok) break;
+        if (mine) values(j, 0);
+        if (more) ok = arrived(2 * j + 2);
+        if (mine) ok = ok && wait(B_P + 2 * i + 1, j - T.from[i]);
+        if (!ok) break;
+        if (mine) values(j, 1);
+        if (mine && j + 1 == T.to[i]) commit_1_elect(bar(B_O + i));
+        commit_1_elect(empty(2 * j + 1));
+        if (sees(j + 1)) scores(j + 1);
         __syncwarp();
         if (lane == 0) mbar_arrive_local(bar(B_TURN + 1 - i));
         __syncwarp();
-      };
-      auto sees = [&](int j) { return j >= T.from[i] && j < T.to[i]; };
-      // scores over K(j), which then has been read by this tile
-      auto scores = [&](int j) {
-        if (!arrived(2 * j)) return false;
-        if (j > 0) pass_turn();
-        if (sees(j)) {
-          tc_fence_after();
-#pragma unroll
-          for (int c = 0; c < C::kQk; ++c)
-            mma_1_x4_elect<2, 2>(tmem + 128u * i, desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024),
-                                 desc_sw128(slot(C::kPer * j + c), 16, 1024), kIdescS, c != 0);
-          commit_1_elect(bar(B_S + i));
-        }
-        commit_1_elect(empty(2 * j));
-        return true;
-      };
-      ok = ok && scores(0);
-      for (int j = 0; ok && j < T.n; ++j) {
-        // in turn: A's products of key tile j, then B's, then A's of the next
-        if (i + j > 0) ok = mbar_wait_converged(bar(B_TURN + i), (i ? j : j - 1) & 1, abort_flag, p.status, wait_ns);
-        ok = ok && arrived(2 * j + 1);
-        if (ok && sees(j)) {
-          const int it = j - T.from[i];
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && mbar_wait_converged(bar(B_P + 2 * i + half), it & 1, abort_flag, p.status, wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            // 16 keys a step: weights in 8 columns, V rows 2 KB further on
-            mma_1_ts_x4_elect<8, 128>(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half,
-                                      desc_sw128(slot(C::kPer * j + C::kQk + half), kChunk / 2, 1024), kIdescPV,
-                                      (it | half) != 0);
-          }
-          if (ok && j + 1 == T.to[i]) commit_1_elect(bar(B_O + i));
-        }
-        if (!ok) break;
-        commit_1_elect(empty(2 * j + 1));
-        if (j + 1 < T.n)
-          ok = scores(j + 1);
-        else
-          pass_turn();
+        if (more) commit_1_elect(empty(2 * j + 2));
       }
       commit_1_elect(bar(B_DRAIN + i));
       int keep = 0;
@@ -400,6 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t cs = 128u * t, co = kTmemO + 128u * t;
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
     float m_used = -CUDART_INF_F, l = 0.f;
+    bool stale = true;  // the reference m_used has to be found (again)
     for (int j = T.from[t]; j < T.to[t]; ++j) {
       if (!mbar_wait_converged(bar(B_S + t), (j - T.from[t]) & 1, abort_flag, p.status, wait_ns)) break;
       tc_fence_after();
@@ -408,9 +406,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < 4; ++c) tmem_ld32(tl + cs + 32u * c, sr[c]);
       tmem_wait_ld();
       const int kb = T.k0 + 128 * j;
+      const bool masked = __any_sync(0xffffffffu, lo > kb || hi < kb + 128);
+      if (masked) {
+        const uint32_t a = (uint32_t)max(lo - kb, 0), n = (uint32_t)max(min(hi - kb, 128) - (int)a, 0);
+#pragma unroll
+        for (int k = 0; k < 128; ++k)
+          if ((uint32_t)k - a >= n) sr[k >> 5][k & 31] = 0xff800000u;
+      }
       auto score = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
-      // four running maxima, joined
-      auto maximum = [&]() {
+      // The weights are 2^(s scale - m) for a reference m near the row's maximum so far,
+      // not the maximum itself: any m gives the same quotient, as long as the weights
+      // and their sums stay within fp32 and bf16's common range.  So m is found where
+      // there is none and raised one tile after a weight went beyond 2^8; the hot loop
+      // takes no maximum.
+      if (__any_sync(0xffffffffu, stale)) {
         float m4[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) m4[k] = score(k);
@@ -420,73 +429,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], score(k + 2 * i), score(k + 2 * i + 1));
         m4[0] = max3(m4[0], score(124), score(125));
         m4[1] = max3(m4[1], score(126), score(127));
-        return max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]) * p.scale_log2;
-      };
-      // weights 2^(s scale - m) of 64 keys, in bf16 pairs; with `kPoly` a part of the
-      // exponentials goes to the FMA pipe
-      uint64_t sum[2] = {0, 0};
-      auto weights = [&](int half, float ref, auto poly, uint32_t (&pk)[32]) {
-        const uint64_t ref2 = pack2(ref, ref);
-#pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int u = 64 * half + 2 * k;
-          const uint64_t x = fma2(pack2(score(u), score(u + 1)), scale2, ref2);
-          float p0, p1;
-          if (decltype(poly)::value && (k & 3) == 3) {
-            exp2_poly2(x, p0, p1);
-          } else {
-            unpack2(x, p0, p1);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-          }
-          sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
-          pk[k] = pack_bf16(p0, p1);
-        }
-      };
-      // over the scores, and to the MMA warp
-      auto hand_over = [&](int half, uint32_t (&pk)[32]) {
-        tmem_st32(tl + cs + 32u * half, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(bar(B_P + 2 * t + half));
-      };
-      const bool masked = __any_sync(0xffffffffu, lo > kb || hi < kb + 128);
-      bool careful = masked || __any_sync(0xffffffffu, m_used == -CUDART_INF_F);
-      if (!careful) {
-        // Most tiles raise no maximum by more than 2^8: the weights of the first half
-        // are formed against the old one while the new one is found.
-        uint32_t pk[32];
-        weights(0, -m_used, Poly<true>(), pk);
-        const float mx = maximum();
-        careful = __any_sync(0xffffffffu, !(mx <= m_used + kRescale));
-        if (!careful) {
-          hand_over(0, pk);
-          weights(1, -m_used, Poly<true>(), pk);
-          hand_over(1, pk);
-        } else {
-          sum[0] = sum[1] = 0;
-        }
-      }
-      if (careful) {
-        if (masked) {
-          const uint32_t a = (uint32_t)max(lo - kb, 0), n = (uint32_t)max(min(hi - kb, 128) - (int)a, 0);
-#pragma unroll
-          for (int k = 0; k < 128; ++k)
-            if ((uint32_t)k - a >= n) sr[k >> 5][k & 31] = 0xff800000u;
-        }
-        const float mx = maximum();
+        float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]) * p.scale_log2;
+        // a NaN or an infinite maximum: the row is done over in fp32 at the end
+        if (!(mx < CUDART_INF_F)) l = CUDART_NAN_F;
+        // the old tiles' largest weight counts as well: l is a bound of it
+        if (l > 1.f) mx = fmaxf(mx, m_used + log2f(l));
         float alpha = 1.f;
         bool resc = false;
-        if (mx > m_used + kRescale) {
+        if (mx > m_used) {
           // (with no weight so far there is nothing to rescale: O holds zeros for this row)
           alpha = ex2_approx(m_used - mx);
           resc = l != 0.f;
           l *= alpha;
           m_used = mx;
         }
-        // a NaN or an infinite maximum: the row is done over in fp32 at the end
-        if (!(mx < CUDART_INF_F)) l = CUDART_NAN_F;
         if (__any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
@@ -499,16 +455,54 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_st();
         }
-        const float ref = m_used == -CUDART_INF_F ? 0.f : -m_used;
+        stale = m_used == -CUDART_INF_F;
+      }
+      const float ref = m_used == -CUDART_INF_F ? 0.f : -m_used;
+      const uint64_t ref2 = pack2(ref, ref);
+      uint64_t sum[2] = {0, 0};
+      float top = 0.f;  // the largest exponent that the polynomial was given
+      // the weights of 64 keys, in bf16 pairs over the scores and to the MMA warp; with
+      // `poly` a part of the exponentials goes to the FMA pipe
+      auto weights = [&](int half, auto poly) {
         uint32_t pk[32];
-        weights(0, ref, Poly<false>(), pk);
-        hand_over(0, pk);
-        weights(1, ref, Poly<false>(), pk);
-        hand_over(1, pk);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const int u = 64 * half + 2 * k;
+          const uint64_t x = fma2(pack2(score(u), score(u + 1)), scale2, ref2);
+          float p0, p1;
+          if (decltype(poly)::value && ((kPolyPairs >> (k & 7)) & 1)) {
+            unpack2(x, p0, p1);
+            top = max3(top, p0, p1);
+            exp2_poly2(x, p0, p1);
+          } else {
+            unpack2(x, p0, p1);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+          }
+          sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
+          pk[k] = pack_bf16(p0, p1);
+        }
+        tmem_st32(tl + cs + 32u * half, pk);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(bar(B_P + 2 * t + half));
+      };
+      if (masked || __any_sync(0xffffffffu, stale)) {
+        // exact zeros for what is not seen
+        weights(0, Poly<false>());
+        weights(1, Poly<false>());
+      } else {
+        weights(0, Poly<true>());
+        weights(1, Poly<true>());
       }
       float s0, s1;
       unpack2(add2(sum[0], sum[1]), s0, s1);
-      l += s0 + s1;
+      const float tile = s0 + s1;
+      l += tile;
+      stale = stale || tile > kRescale;
+      // beyond 2^60 (a NaN included) within one tile: the row is done over as well
+      if (!(tile < kBeyond && top < 60.f)) l = CUDART_NAN_F;
     }
     // ---- o = O / l, lse
     const bool any = T.to[t] > T.from[t];
