@@ -37,18 +37,12 @@ MLA_DEVI PackedSeq packed_find(const int32_t* cu, int B, int n_tok, int t, int l
   return s;
 }
 
-// Rows [lo, hi) of the sequence that row first + lane belongs to (lo = hi = 0: none),
-// for the 32 rows of a warp: one search for the first of them; lanes beyond that
-// sequence's end search the offsets behind it.
+// Rows [lo, hi) of the sequence that this thread's row t belongs to (lo = hi = 0: none).
 struct PackedRow {
   int lo, hi;
 };
-MLA_DEVI PackedRow packed_row(const int32_t* cu, int B, int n_tok, int first, int lane) {
-  const PackedSeq s = packed_find(cu, B, n_tok, first, lane);
-  const int t = first + lane;
-  if (s.b >= 0 && t < s.hi) return {s.lo, s.hi};
-  if (t >= n_tok) return {0, 0};
-  int a = s.b >= 0 ? s.b + 1 : 0, z = B;  // the count of entries cu[1 .. B] that are <= t
+MLA_DEVI PackedRow packed_own(const int32_t* cu, int B, int n_tok, int t) {
+  int a = 0, z = B;  // the count of entries cu[1 .. B] that are <= t
   while (a < z) {
     const int mid = a + (z - a) / 2;
     if (cu[mid + 1] <= t)

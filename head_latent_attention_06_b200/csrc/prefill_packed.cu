@@ -26,7 +26,7 @@ struct PackedParams {
   float* lse;
   uint32_t* status;
   int64_t qn_tok, qn_head, qp_tok, qp_head, kn_tok, kn_head, kp_tok, v_tok, v_head;
-  int n_tok, B, H, share, causal, blocks;
+  int n_tok, B, H, share, causal, blocks, wide, group, sorted;
   float scale_log2;
   uint64_t wait_ns;
 };
@@ -97,25 +97,25 @@ MLA_DEVI void attend_row(const PackedParams& p, int t, int h, int lo, int hi, in
 }
 
 // ---------------------------------------------------------------- tiles
-constexpr int kThreads = 384;               // warp 0 loads, warps 1 and 2 MMA, warps 4..7 tile A, 8..11 tile B
-constexpr int kRows = 256;                  // packed rows of a CTA: tile A the first 128, B the others
+constexpr int kThreads = 384;               // warp 0 loads, 1 and 2 MMA, 3 plans, 4..7 tile A, 8..11 tile B
+constexpr int kRows = 256;                  // packed rows of a block: tile A the first 128, B the others
 constexpr uint32_t kChunk = 128 * 128;      // 16 KB: 128 rows x 64 values, or 64 keys x 128 values
-constexpr int kHeadGroup = 8;               // heads whose blocks run side by side
+constexpr int kHeadGroup = 16;              // key and value heads whose blocks run side by side
+constexpr int kMaxSorted = 128;             // blocks of rows that are put in order of their work
 
 template <bool PE>
 struct Cfg {
   static constexpr int kQk = PE ? 3 : 2;              // 64-value chunks of a query or key
   static constexpr int kSlots = PE ? 8 : 10;          // ring of K and V chunks
   static constexpr int kPer = kQk + 2;                // chunks of one key tile: K, then V in halves of 64 keys
-  // K(j) may go in once the item kWaitK before it has been read, V(j) once the item
-  // kWaitV before it has: with 8 slots of which a key tile takes 3 + 2, K(j) ends at 5 j + 3
-  // and needs V(j - 2), which ends at 5 j - 5, gone; V(j) ends at 5 j + 5 and needs
-  // K(j - 1), which ends at 5 j - 2, gone.  With 10 slots of 2 + 2, K(j) needs 4 j - 8
-  // (V(j - 3)) and V(j) 4 j - 6 (K(j - 2)).
-  static constexpr int kWaitK = PE ? 3 : 5, kWaitV = PE ? 3 : 5;
+  // K(j) may go in once the item kWait before it has been read, V(j) likewise: with 8
+  // slots of which a key tile takes 3 + 2, K(j) ends at 5 j + 3 and needs V(j - 2), which
+  // ends at 5 j - 5, gone; V(j) ends at 5 j + 5 and needs K(j - 1), which ends at 5 j - 2,
+  // gone.  With 10 slots of 2 + 2, K(j) needs 4 j - 8 (V(j - 3)) and V(j) 4 j - 6 (K(j - 2)).
+  static constexpr int kWait = PE ? 3 : 5;
   static constexpr uint32_t kRing = 2 * kQk * kChunk;
   static constexpr uint32_t kBars = kRing + kSlots * kChunk;
-  static constexpr uint32_t kSmem = kBars + 512 + 1024;
+  static constexpr uint32_t kSmem = kBars + 1024 + 1024;
 };
 static_assert(Cfg<true>::kSmem <= 232448 && Cfg<false>::kSmem <= 232448, "shared memory budget");
 
@@ -125,19 +125,26 @@ constexpr uint32_t kIdescS = idesc_bf16_f32(128, 128, false, false);
 constexpr uint32_t kIdescPV = idesc_bf16_f32(128, 128, false, true);
 constexpr float kRescale = 256.f;             // a tile's weights beyond this ask for a new reference
 constexpr float kBeyond = 1.152921504606847e18f;  // 2^60: no range is left to wait for it
-constexpr int kPolyPairs = 0x00;              // of eight pairs of exponentials, those on the FMA pipe
-// barriers; [2] per tile, P[2 t + half]
-constexpr int B_Q = 0, B_S = 1, B_P = 3, B_O = 7, B_DRAIN = 9, B_FULL = 11, B_EMPTY = 19, B_TURN = 27, B_COUNT = 29;
+// Barriers.  [2] per query tile: its queries are in / have been read, its scores are
+// there, its output is there / has been read; P [2 t + half] its weights; [8] per ring
+// item in turn; [2] per plan in turn.
+constexpr int B_Q = 0, B_READ_Q = 2, B_S = 4, B_P = 6, B_O = 10, B_READ_O = 12, B_TURN = 14, B_DRAIN = 16, B_FULL = 18,
+              B_EMPTY = 26, B_PLAN = 34, B_READ_PLAN = 36, B_NEXT = 38, B_BEGUN = 39, B_COUNT = 40;
+// behind the barriers: the answer of the launch control, words, two plans
+constexpr uint32_t kNextOff = 320, kWordsOff = 336, kPlanOff = 384;
 
-struct Tiles {
-  int k0;         // first key of the block's first key tile
-  int n;          // key tiles
+// What a block of rows and a head needs, as the planning warp leaves it.
+struct Plan {
+  int h, q0;           // head (-1: no more work) and first row
+  int k0, n;           // first key of the block's first key tile, key tiles
   int from[2], to[2];  // those of them that query tile A and B see
+  // per 32 rows: those of a sequence, the first one's first key and its sequence's end,
+  // whether all are of that sequence
+  int first[8], last[8], lo[8], hi[8], one[8];
 };
+constexpr uint32_t kOrderOff = kPlanOff + 2 * sizeof(Plan);
+static_assert(kOrderOff + kMaxSorted <= 1024 && kWordsOff + 48 <= kPlanOff && 8 * B_COUNT <= kNextOff, "layout");
 
-// 2^x by a polynomial on the FMA pipe: x = n + f, |f| <= 1/2, 2^f by the degree-4
-// minimax polynomial of relative error 2.6e-6 (its coefficients come out of a Remez
-// exchange), the exponent n added to the bits.  For finite x >= -126.
 MLA_DEVI uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -154,28 +161,32 @@ MLA_DEVI uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-MLA_DEVI void exp2_poly2(uint64_t x, float& p0, float& p1) {
-  float x0, x1;
-  unpack2(x, x0, x1);
-  x = pack2(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const float kMagic = 12582912.f;  // 1.5 * 2^23: adding it leaves round(x) in the low mantissa bits
-  const uint64_t t = add2(x, pack2(kMagic, kMagic));
-  const uint64_t f = fma2(add2(t, pack2(-kMagic, -kMagic)), pack2(-1.f, -1.f), x);
-  uint64_t r = pack2(0.009570102207362652f, 0.009570102207362652f);
-  r = fma2(r, f, pack2(0.05591785907745361f, 0.05591785907745361f));
-  r = fma2(r, f, pack2(0.240247443318367f, 0.240247443318367f));
-  r = fma2(r, f, pack2(0.6931217908859253f, 0.6931217908859253f));
-  r = fma2(r, f, pack2(0.9999992847442627f, 0.9999992847442627f));
-  unpack2(r, p0, p1);
-  float t0, t1;
-  unpack2(t, t0, t1);
-  p0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-  p1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+// The next block that has not been started, asked of the launch control: written to
+// `answer` (16 bytes, counted on `bar`), read by next_block (negative: there is none).
+MLA_DEVI void ask_next(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
 }
-template <bool kOn>
-struct Poly {
-  static constexpr bool value = kOn;
-};
+MLA_DEVI int next_block(uint32_t answer) {
+  int x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%1];\n\t"
+      "mov.s32 %0, -1;\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(x)
+      : "r"(answer)
+      : "memory");
+  return x;
+}
+// 32 bytes to global memory
+MLA_DEVI void stg256(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
 // maximum of three that keeps a NaN
 MLA_DEVI float max3(float a, float b, float c) {
   float r;
@@ -193,43 +204,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t sa = (raw + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (sa - raw);
-  // warp-uniform, and known to be: what the MMA warp computes stays in uniform registers
+  // warp-uniform, and known to be: what the MMA warps compute stays in uniform registers
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto bar = [&](int i) -> uint32_t { return sa + C::kBars + 8u * i; };
-  auto full = [&](int item) -> uint32_t { return bar(B_FULL + (item & 7)); };
-  auto empty = [&](int item) -> uint32_t { return bar(B_EMPTY + (item & 7)); };
   auto slot = [&](int s) -> uint32_t { return sa + C::kRing + (s % C::kSlots) * kChunk; };
-  int* words = reinterpret_cast<int*>(sm + C::kBars + 8 * B_COUNT);
+  int* words = reinterpret_cast<int*>(sm + C::kBars + kWordsOff);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   volatile int* abort_flag = words + 1;
-  int* issued = words + 2;
-  int* low = words + 4;    // [8] per softmax warp: the first key its rows see
-  int* high = words + 12;  // [8] one past the last
-
-  // blocks of a group of heads in turn, the last rows (the longest, when causal) first
-  const int per_group = kHeadGroup * p.blocks;
-  const int grp = blockIdx.x / per_group, in = blockIdx.x - grp * per_group;
-  const int gh = min(kHeadGroup, p.H - grp * kHeadGroup);
-  const int blk = p.blocks - 1 - in / gh, h = grp * kHeadGroup + in % gh;
-  const int g = h / p.share;
-  const int q0 = blk * kRows;
+  int* issued = words + 2;  // ring items, queries of tile A, of B
+  Plan* plans = reinterpret_cast<Plan*>(sm + C::kBars + kPlanOff);
   const uint64_t wait_ns = p.wait_ns;
+  auto wait = [&](int b, int parity) { return mbar_wait_converged(bar(b), parity & 1, abort_flag, p.status, wait_ns); };
+  auto arrive = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive_local(bar(b));
+    __syncwarp();
+  };
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    *issued = 0;
-    mbar_init(bar(B_Q), 1);
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(bar(B_S + t), 1);
-      mbar_init(bar(B_P + 2 * t), 4);
-      mbar_init(bar(B_P + 2 * t + 1), 4);
-      mbar_init(bar(B_O + t), 1);
-      mbar_init(bar(B_DRAIN + t), 1);
-      mbar_init(bar(B_TURN + t), 1);
-    }
-    for (int i = 0; i < 8; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), 2);  // both query tiles have read it
+    issued[0] = issued[1] = issued[2] = 0;
+    for (int i = 0; i < B_COUNT; ++i) {
+      int count = 1;
+      if ((i >= B_P && i < B_P + 4) || (i >= B_READ_O && i < B_READ_O + 2)) count = 4;  // a softmax warp each
+      if (i >= B_EMPTY && i < B_EMPTY + 8) count = 2;                                    // both MMA warps
+      if (i >= B_READ_PLAN && i < B_READ_PLAN + 2) count = 11;                           // all warps but the planning one
+      mbar_init(bar(i), count);
     }
     fence_mbar_init();
   }
@@ -237,329 +237,480 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc_1(smem_u32(tmem_slot), 512);
     tmem_relinquish_1();
   }
-  pdl_trigger();
-  pdl_wait();
-  // ---- the keys of every row: of its own prompt, up to itself when causal
-  const int t = (warp - 4) >> 2;                          // query tile of a softmax warp
-  const int row = 32 * (warp & 3) + lane;                 // its TMEM lane
-  const int qi = q0 + 128 * t + row;
-  int lo = 0, hi = 0;
-  if (warp >= 4) {
-    const int first = q0 + 128 * t + 32 * (warp & 3);
-    if (first < p.n_tok) {
-      const PackedRow r = packed_row(p.cu, p.B, p.n_tok, first, lane);
-      lo = r.lo;
-      hi = r.hi;
-      if (p.causal && hi > lo) hi = qi + 1;
-    }
-    const int a = __reduce_min_sync(0xffffffffu, hi > lo ? lo : 0x7fffffff);
-    const int z = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) {
-      low[warp - 4] = a;
-      high[warp - 4] = z;
-    }
-  } else if (blockIdx.x == 0 && warp >= 2) {
-    packed_check(p.cu, p.B, p.n_tok, p.status, threadIdx.x - 64, 64);
-  } else if (warp == 0 && lane == 0) {
-    // both tiles' queries (rows past the end read as zeros)
-    mbar_arrive_expect_tx_local(bar(B_Q), 2 * C::kQk * kChunk);
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t dst = sa + i * C::kQk * kChunk;
-      tma_load_3d_cta(dst, &tm_qn, bar(B_Q), 0, h, q0 + 128 * i);
-      tma_load_3d_cta(dst + kChunk, &tm_qn, bar(B_Q), 64, h, q0 + 128 * i);
-      if constexpr (PE) tma_load_3d_cta(dst + 2 * kChunk, &tm_qp, bar(B_Q), 0, h, q0 + 128 * i);
-    }
-  }
-  __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  Tiles T;
-  {
-    int a[2], z[2];
-    for (int i = 0; i < 2; ++i) {
-      a[i] = min(min(low[4 * i], low[4 * i + 1]), min(low[4 * i + 2], low[4 * i + 3]));
-      z[i] = max(max(high[4 * i], high[4 * i + 1]), max(high[4 * i + 2], high[4 * i + 3]));
-    }
-    T.k0 = min(a[0], a[1]);
-    T.n = 0;
-    for (int i = 0; i < 2; ++i) {
-      const bool any = z[i] > a[i];
-      T.from[i] = any ? (a[i] - T.k0) / 128 : 0;
-      T.to[i] = any ? (z[i] - T.k0 + 127) / 128 : 0;
-      T.n = max(T.n, T.to[i]);
-    }
-  }
+  pdl_wait();
 
-  // 384 threads launched with 168 registers: 128 x 80 + 256 x 208 is within that
+  // Every warp goes through the same plans, its own counters running on from one to
+  // the next; a barrier's phase is the count of its uses.  One warp loads, so the
+  // next block's keys and queries come in under the last block's tail, and its first
+  // scores are formed under the last one's output.
   if (warp < 4) {
-    regs_dec<80>();
-    if (warp == 0) {
-    // =========================== loads ===========================
-    // Items in the ring, each with a full and an empty barrier of eight taken in turn:
-    // K(j) is item 2 j (kQk slots from kPer j on), V(j) item 2 j + 1 (two slots after
-    // it).  An item goes into slots whose last holders have been read: see Cfg::kWaitK.
-    int count = 0;
-    bool ok = true;
-    for (int j = 0; ok && j < T.n; ++j) {
-      const int key = T.k0 + 128 * j;
+    regs_dec<80>();  // 384 threads launched with 168 registers: 128 x 80 + 256 x 208 is within that
+    if (warp == 3) {
+      // =========================== plans ===========================
+      if (blockIdx.x == 0) packed_check(p.cu, p.B, p.n_tok, p.status, lane, 32);
+      const uint32_t answer = sa + C::kBars + kNextOff;
+      const int cu0 = min(max(p.cu[0], 0), p.n_tok), cu1 = min(max(p.cu[p.B], 0), p.n_tok);
+      // the sequence of row r, for rows [cu0, cu1): its bounds
+      auto find = [&](int r, int& lo, int& hi) {
+        int a = 0, z = p.B;  // the count of entries cu[1 .. B] that are <= r
+        while (a < z) {
+          const int mid = a + (z - a) / 2;
+          if (p.cu[mid + 1] <= r)
+            a = mid + 1;
+          else
+            z = mid;
+        }
+        a = min(a, p.B - 1);
+        lo = min(max(p.cu[a], 0), r);
+        hi = max(min(p.cu[a + 1], p.n_tok), r + 1);
+      };
+      uint8_t* order = sm + C::kBars + kOrderOff;
+      if (p.sorted) {
+        // the blocks by falling number of key tiles, so that the last ones to be taken are short
+        int mine[kMaxSorted / 32], rank[kMaxSorted / 32];
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        const int item = 2 * j + v, last = item - (v ? C::kWaitV : C::kWaitK);
-        if (last >= 0) ok = ok && mbar_wait_converged(empty(last), (last >> 3) & 1, abort_flag, p.status, wait_ns);
-        if (!ok) break;
-        if (lane == 0) {
-          const uint32_t f = full(item);
-          const int s = C::kPer * j + (v ? C::kQk : 0);
-          mbar_arrive_expect_tx_local(f, (v ? 2 : C::kQk) * kChunk);
-          if (v == 0) {
-            tma_load_3d_cta(slot(s), &tm_kn, f, 0, g, key);
-            tma_load_3d_cta(slot(s + 1), &tm_kn, f, 64, g, key);
-            if constexpr (PE) tma_load_3d_cta(slot(s + 2), &tm_kp, f, 0, 0, key);
-          } else {
-            // halves of 64 keys, 128 values each
-            for (int half = 0; half < 2; ++half) {
-              tma_load_3d_cta(slot(s + half), &tm_v, f, 0, g, key + 64 * half);
-              tma_load_3d_cta(slot(s + half) + kChunk / 2, &tm_v, f, 64, g, key + 64 * half);
-            }
+        for (int k = 0; k < kMaxSorted / 32; ++k) {
+          const int b = lane + 32 * k, first = max(b * kRows, cu0), last = min(b * kRows + kRows, cu1) - 1;
+          mine[k] = b < p.blocks ? 0 : -1;
+          rank[k] = 0;
+          if (b < p.blocks && first <= last) {
+            int lo, hi, lo2;
+            find(first, lo, hi);
+            hi = last + 1;
+            if (!p.causal) find(last, lo2, hi);
+            mine[k] = (hi - lo + 127) >> 7;
           }
         }
         __syncwarp();
-        count = item + 1;
-      }
-    }
-    if (lane == 0) *issued = count;
-  } else if (warp < 3) {
-    // =========================== MMA issue ===========================
-    // One warp per query tile: P.V, then the next scores, while the other tile's
-    // softmax runs under them.  (One warp for both issued 40 MMAs, six waits and four
-    // commits per key tile, 3500 cycles of it, more than the 2560 that the tensor pipe
-    // needs.)  The pipe takes a warp's products in order, so scores may follow the P.V
-    // that reads the weights they overwrite without a wait between the two.
-    const int i = warp - 1;
-    if (T.n > 0) {
-      bool ok = mbar_wait_converged(bar(B_Q), 0, abort_flag, p.status, wait_ns);
-      auto wait = [&](int b, int parity) { return mbar_wait_converged(bar(b), parity & 1, abort_flag, p.status, wait_ns); };
-      auto arrived = [&](int item) { return wait(B_FULL + (item & 7), item >> 3); };
-      auto sees = [&](int j) { return j >= T.from[i] && j < T.to[i]; };
-      // scores over K(j)
-      auto scores = [&](int j) {
-        tc_fence_after();
 #pragma unroll
-        for (int c = 0; c < C::kQk; ++c)
-          mma_1_x4_elect<2, 2>(tmem + 128u * i, desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024),
-                               desc_sw128(slot(C::kPer * j + c), 16, 1024), kIdescS, c != 0);
-        commit_1_elect(bar(B_S + i));
-      };
-      // the weights of half a key tile times V(j): 16 keys a step, weights in 8 columns, V
-      // rows 2 KB further on
-      auto values = [&](int j, int half) {
-        tc_fence_after();
-        mma_1_ts_x4_elect<8, 128>(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half,
-                                  desc_sw128(slot(C::kPer * j + C::kQk + half), kChunk / 2, 1024), kIdescPV,
-                                  (j > T.from[i] || half) ? 1u : 0u);
-      };
-      ok = ok && arrived(0);
-      if (ok) {
-        if (sees(0)) scores(0);
-        commit_1_elect(empty(0));
+        for (int k = 0; k < kMaxSorted / 32; ++k)
+          for (int l = 0; l < 32 && 32 * k + l < p.blocks; ++l) {
+            const int other = __shfl_sync(0xffffffffu, mine[k], l), b = 32 * k + l;
+#pragma unroll
+            for (int m = 0; m < kMaxSorted / 32; ++m) rank[m] += other > mine[m] || (other == mine[m] && b < lane + 32 * m);
+          }
+#pragma unroll
+        for (int k = 0; k < kMaxSorted / 32; ++k)
+          if (lane + 32 * k < p.blocks) order[rank[k]] = (uint8_t)(lane + 32 * k);
+        __syncwarp();
       }
-      for (int j = 0; ok && j < T.n; ++j) {
-        const bool mine = sees(j), more = j + 1 < T.n;
-        ok = arrived(2 * j + 1);
-        if (mine) ok = ok && wait(B_P + 2 * i, j - T.from[i]);
-        // in turn: A's products of key tile j, then B's, then A's of the next
-        if (i + j > 0) ok = ok && wait(B_TURN + i, i ? j : j - 1);
-        if (!ok) break;
-        if (mine) values(j, 0);
-        if (more) ok = arrived(2 * j + 2);
-        if (mine) ok = ok && wait(B_P + 2 * i + 1, j - T.from[i]);
-        if (!ok) break;
-        if (mine) values(j, 1);
-        if (mine && j + 1 == T.to[i]) commit_1_elect(bar(B_O + i));
-        commit_1_elect(empty(2 * j + 1));
-        if (sees(j + 1)) scores(j + 1);
+      int block = blockIdx.x;
+      for (int w = 0;; ++w) {
+        if (w >= 2 && !wait(B_READ_PLAN + (w & 1), (w >> 1) - 1)) break;
+        Plan* pl = plans + (w & 1);
+        if (block < 0) {
+          if (lane == 0) pl->h = -1;
+          arrive(B_PLAN + (w & 1));
+          break;
+        }
+        // groups of heads whose keys and values L2 holds; in a group all heads of the
+        // longest block first (unsorted: of the last rows, the longest when causal)
+        const int per_group = p.group * p.blocks;
+        const int grp = block / per_group, in = block - grp * per_group;
+        const int gh = min(p.group, p.H - grp * p.group);
+        const int h = grp * p.group + in % gh, at = in / gh;
+        const int q0 = (p.sorted ? order[at] : p.blocks - 1 - at) * kRows;
+        // lanes 0 .. 7: the first row of 32 that is in a sequence; lanes 8 .. 15: the last
+        const int base = q0 + 32 * (lane & 7);
+        const int first = max(base, cu0), last = min(base + 31, cu1 - 1);
+        const int r = lane & 8 ? last : first;
+        int lo = 0, hi = 0;
+        const bool any = first <= last;
+        if (any && lane < 16) find(r, lo, hi);
         __syncwarp();
-        if (lane == 0) mbar_arrive_local(bar(B_TURN + 1 - i));
+        const int lo_last = __shfl_sync(0xffffffffu, lo, (lane & 7) + 8);
+        const int hi_last = __shfl_sync(0xffffffffu, hi, (lane & 7) + 8);
+        int kl = any ? lo : 0x7fffffff, kh = any ? (p.causal ? last + 1 : hi_last) : 0;
+        for (int o = 1; o < 4; o <<= 1) {
+          kl = min(kl, __shfl_xor_sync(0xffffffffu, kl, o));
+          kh = max(kh, __shfl_xor_sync(0xffffffffu, kh, o));
+        }
+        const int kl_a = __shfl_sync(0xffffffffu, kl, 0), kl_b = __shfl_sync(0xffffffffu, kl, 4);
+        const int kh_a = __shfl_sync(0xffffffffu, kh, 0), kh_b = __shfl_sync(0xffffffffu, kh, 4);
+        if (lane < 8) {
+          pl->first[lane] = any ? first : 0;
+          pl->last[lane] = any ? last : -1;
+          pl->lo[lane] = lo;
+          pl->hi[lane] = hi;
+          pl->one[lane] = lo == lo_last && last < hi;
+        }
+        const int k0 = min(kl_a, kl_b);
+        if (lane == 0) {
+          pl->h = h;
+          pl->q0 = q0;
+          pl->k0 = k0;
+          pl->from[0] = kh_a > kl_a ? (kl_a - k0) / 128 : 0;
+          pl->to[0] = kh_a > kl_a ? (kh_a - k0 + 127) / 128 : 0;
+          pl->from[1] = kh_b > kl_b ? (kl_b - k0) / 128 : 0;
+          pl->to[1] = kh_b > kl_b ? (kh_b - k0 + 127) / 128 : 0;
+          pl->n = max(pl->to[0], pl->to[1]);
+        }
+        arrive(B_PLAN + (w & 1));
+        // The next block is claimed when the loads of this one begin, not before: a block
+        // held in store is one that an idle SM cannot take.
+        if (!wait(B_BEGUN, w)) break;
+        if (lane == 0) {
+          fence_proxy_async_smem();  // the last answer has been read
+          mbar_arrive_expect_tx_local(bar(B_NEXT), 16);
+          ask_next(answer, bar(B_NEXT));
+        }
         __syncwarp();
-        if (more) commit_1_elect(empty(2 * j + 2));
+        if (!wait(B_NEXT, w)) {
+          int give_up = 0;  // the answer must not outlive the block
+          mbar_wait_converged(bar(B_NEXT), w & 1, &give_up, nullptr, kDrainNs);
+          break;
+        }
+        block = next_block(answer);
+      }
+    } else if (warp == 0) {
+      // =========================== loads ===========================
+      // Items in the ring, each with a full and an empty barrier of eight taken in turn:
+      // a key tile's K is item 2 j (kQk slots), its V item 2 j + 1 (two slots), j counting
+      // the key tiles of all blocks.
+      bool ok = true;
+      int jj = 0, nq[2] = {0, 0};
+      for (int w = 0; ok; ++w) {
+        if (!wait(B_PLAN + (w & 1), w >> 1)) break;
+        const Plan* pl = plans + (w & 1);
+        const int h = pl->h, q0 = pl->q0, k0 = pl->k0, n = pl->n;
+        const bool on[2] = {pl->to[0] > pl->from[0], pl->to[1] > pl->from[1]};
+        arrive(B_READ_PLAN + (w & 1));
+        if (h < 0) break;
+        arrive(B_BEGUN);
+        const int g = h / p.share;
+        auto item = [&](int j, int v) {
+          const int it = 2 * (jj + j) + v, old = it - C::kWait, key = k0 + 128 * j;
+          if (old >= 0 && !wait(B_EMPTY + (old & 7), old >> 3)) return false;
+          if (lane == 0) {
+            const uint32_t f = bar(B_FULL + (it & 7));
+            const int s = C::kPer * (jj + j) + (v ? C::kQk : 0);
+            mbar_arrive_expect_tx_local(f, (v ? 2 : C::kQk) * kChunk);
+            if (v == 0) {
+              tma_load_3d_cta(slot(s), &tm_kn, f, 0, g, key);
+              tma_load_3d_cta(slot(s + 1), &tm_kn, f, 64, g, key);
+              if constexpr (PE) tma_load_3d_cta(slot(s + 2), &tm_kp, f, 0, 0, key);
+            } else {
+              // halves of 64 keys, 128 values each
+              for (int half = 0; half < 2; ++half) {
+                tma_load_3d_cta(slot(s + half), &tm_v, f, 0, g, key + 64 * half);
+                tma_load_3d_cta(slot(s + half) + kChunk / 2, &tm_v, f, 64, g, key + 64 * half);
+              }
+            }
+            issued[0] = it + 1;
+          }
+          __syncwarp();
+          return true;
+        };
+        if (n > 0) ok = item(0, 0);
+        for (int i = 0; ok && i < 2; ++i) {
+          if (!on[i]) continue;
+          if (nq[i] > 0) ok = wait(B_READ_Q + i, nq[i] - 1);
+          if (!ok) break;
+          ++nq[i];
+          if (lane == 0) {
+            // (rows past the end read as zeros)
+            const uint32_t dst = sa + i * C::kQk * kChunk;
+            mbar_arrive_expect_tx_local(bar(B_Q + i), C::kQk * kChunk);
+            tma_load_3d_cta(dst, &tm_qn, bar(B_Q + i), 0, h, q0 + 128 * i);
+            tma_load_3d_cta(dst + kChunk, &tm_qn, bar(B_Q + i), 64, h, q0 + 128 * i);
+            if constexpr (PE) tma_load_3d_cta(dst + 2 * kChunk, &tm_qp, bar(B_Q + i), 0, h, q0 + 128 * i);
+            issued[1 + i] = nq[i];
+          }
+          __syncwarp();
+        }
+        for (int j = 0; ok && j < n; ++j) {
+          if (j > 0) ok = item(j, 0);
+          if (ok) ok = item(j, 1);
+        }
+        jj += n;
+      }
+    } else {
+      // =========================== MMA issue ===========================
+      // One warp per query tile: P.V, then the next scores, while the other tile's
+      // softmax runs under them.  (One warp for both issued 40 MMAs, six waits and four
+      // commits per key tile, 3500 cycles of it, more than the 2560 that the tensor pipe
+      // needs.)  The pipe takes a warp's products in order, so scores may follow the P.V
+      // that reads the weights they overwrite without a wait between the two.
+      const int i = warp - 1;
+      bool ok = true;
+      int jj = 0, its = 0, nq = 0;  // key tiles of all blocks, those seen, blocks with rows
+      for (int w = 0; ok; ++w) {
+        if (!wait(B_PLAN + (w & 1), w >> 1)) break;
+        const Plan* pl = plans + (w & 1);
+        const int h = pl->h, n = pl->n, from = pl->from[i], to = pl->to[i];
+        arrive(B_READ_PLAN + (w & 1));
+        if (h < 0) break;
+        if (n == 0) continue;
+        auto arrived = [&](int j, int v) {
+          const int it = 2 * (jj + j) + v;
+          return wait(B_FULL + (it & 7), it >> 3);
+        };
+        auto release = [&](int j, int v) { commit_1_elect(bar(B_EMPTY + ((2 * (jj + j) + v) & 7))); };
+        auto sees = [&](int j) { return j >= from && j < to; };
+        // scores over the block's K(j)
+        auto scores = [&](int j) {
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < C::kQk; ++c)
+            mma_1_x4_elect<2, 2>(tmem + 128u * i, desc_sw128(sa + (i * C::kQk + c) * kChunk, 16, 1024),
+                                 desc_sw128(slot(C::kPer * (jj + j) + c), 16, 1024), kIdescS, c != 0);
+          commit_1_elect(bar(B_S + i));
+          if (j + 1 == to) commit_1_elect(bar(B_READ_Q + i));
+        };
+        // the weights of half a key tile times V(j): 16 keys a step, weights in 8 columns, V
+        // rows 2 KB further on
+        auto values = [&](int j, int half) {
+          tc_fence_after();
+          mma_1_ts_x4_elect<8, 128>(tmem + kTmemO + 128u * i, tmem + 128u * i + 32u * half,
+                                    desc_sw128(slot(C::kPer * (jj + j) + C::kQk + half), kChunk / 2, 1024), kIdescPV,
+                                    (j > from || half) ? 1u : 0u);
+        };
+        if (to > from) ok = wait(B_Q + i, nq);
+        ok = ok && arrived(0, 0);
+        if (!ok) break;
+        if (sees(0)) scores(0);
+        release(0, 0);
+        for (int j = 0; ok && j < n; ++j) {
+          const bool mine = sees(j), more = j + 1 < n;
+          ok = arrived(j, 1);
+          // the last block's output has been read
+          if (mine && j == from && nq > 0) ok = ok && wait(B_READ_O + i, nq - 1);
+          if (mine) ok = ok && wait(B_P + 2 * i, its);
+          // in turn: A's products of key tile j, then B's, then A's of the next
+          if (i + jj + j > 0) ok = ok && wait(B_TURN + i, i ? jj + j : jj + j - 1);
+          if (!ok) break;
+          if (mine) values(j, 0);
+          if (more) ok = arrived(j + 1, 0);
+          if (mine) ok = ok && wait(B_P + 2 * i + 1, its);
+          if (!ok) break;
+          if (mine) {
+            values(j, 1);
+            ++its;
+            if (j + 1 == to) commit_1_elect(bar(B_O + i));
+          }
+          release(j, 1);
+          if (sees(j + 1)) scores(j + 1);
+          arrive(B_TURN + 1 - i);
+          if (more) release(j + 1, 0);
+        }
+        jj += n;
+        if (to > from) ++nq;
       }
       commit_1_elect(bar(B_DRAIN + i));
       int keep = 0;
       mbar_wait_converged(bar(B_DRAIN + i), 0, &keep, p.status, kDrainNs);
     }
-  }
   } else {
     regs_inc<208>();
     // ================ softmax: a thread per query row ================
+    const int t = (warp - 4) >> 2;                     // query tile
+    const int row = 32 * (warp & 3) + lane;            // its TMEM lane
+    const int grp = 4 * t + (warp & 3);
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t cs = 128u * t, co = kTmemO + 128u * t;
     const uint64_t scale2 = pack2(p.scale_log2, p.scale_log2);
-    float m_used = -CUDART_INF_F, l = 0.f;
-    bool stale = true;  // the reference m_used has to be found (again)
-    for (int j = T.from[t]; j < T.to[t]; ++j) {
-      if (!mbar_wait_converged(bar(B_S + t), (j - T.from[t]) & 1, abort_flag, p.status, wait_ns)) break;
-      tc_fence_after();
-      uint32_t sr[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(tl + cs + 32u * c, sr[c]);
-      tmem_wait_ld();
-      const int kb = T.k0 + 128 * j;
-      const bool masked = __any_sync(0xffffffffu, lo > kb || hi < kb + 128);
-      if (masked) {
-        const uint32_t a = (uint32_t)max(lo - kb, 0), n = (uint32_t)max(min(hi - kb, 128) - (int)a, 0);
-#pragma unroll
-        for (int k = 0; k < 128; ++k)
-          if ((uint32_t)k - a >= n) sr[k >> 5][k & 31] = 0xff800000u;
-      }
-      auto score = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
-      // The weights are 2^(s scale - m) for a reference m near the row's maximum so far,
-      // not the maximum itself: any m gives the same quotient, as long as the weights
-      // and their sums stay within fp32 and bf16's common range.  So m is found where
-      // there is none and raised one tile after a weight went beyond 2^8; the hot loop
-      // takes no maximum.
-      if (__any_sync(0xffffffffu, stale)) {
-        float m4[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) m4[k] = score(k);
-#pragma unroll
-        for (int k = 4; k < 124; k += 8)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], score(k + 2 * i), score(k + 2 * i + 1));
-        m4[0] = max3(m4[0], score(124), score(125));
-        m4[1] = max3(m4[1], score(126), score(127));
-        float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]) * p.scale_log2;
-        // a NaN or an infinite maximum: the row is done over in fp32 at the end
-        if (!(mx < CUDART_INF_F)) l = CUDART_NAN_F;
-        // the old tiles' largest weight counts as well: l is a bound of it
-        if (l > 1.f) mx = fmaxf(mx, m_used + log2f(l));
-        float alpha = 1.f;
-        bool resc = false;
-        if (mx > m_used) {
-          // (with no weight so far there is nothing to rescale: O holds zeros for this row)
-          alpha = ex2_approx(m_used - mx);
-          resc = l != 0.f;
-          l *= alpha;
-          m_used = mx;
+    bool ok = true;
+    int its = 0, nq = 0;
+    for (int w = 0; ok; ++w) {
+      if (!wait(B_PLAN + (w & 1), w >> 1)) break;
+      const Plan* pl = plans + (w & 1);
+      const int h = pl->h, k0 = pl->k0, from = pl->from[t], to = pl->to[t];
+      const int qi = pl->q0 + 128 * t + row;
+      // the keys of this row: of its own sequence, up to itself when causal
+      int lo = 0, hi = 0;
+      if (h >= 0 && qi >= pl->first[grp] && qi <= pl->last[grp]) {
+        lo = pl->lo[grp];
+        hi = pl->hi[grp];
+        if (!pl->one[grp]) {
+          const PackedRow r = packed_own(p.cu, p.B, p.n_tok, qi);
+          lo = r.lo;
+          hi = r.hi;
         }
-        if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tl + co + 32u * c, o);
-            tmem_wait_ld();
+        if (p.causal && hi > lo) hi = qi + 1;
+      }
+      arrive(B_READ_PLAN + (w & 1));
+      if (h < 0) break;
+      if (to <= from) continue;
+      float m_used = -CUDART_INF_F, l = 0.f;
+      bool stale = true;  // the reference m_used has to be found (again)
+      for (int j = from; j < to; ++j, ++its) {
+        ok = wait(B_S + t, its);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[4][32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            tmem_st32(tl + co + 32u * c, o);
+        for (int c = 0; c < 4; ++c) tmem_ld32(tl + cs + 32u * c, sr[c]);
+        tmem_wait_ld();
+        const int kb = k0 + 128 * j;
+        if (__any_sync(0xffffffffu, lo > kb || hi < kb + 128)) {
+          const uint32_t a = (uint32_t)max(lo - kb, 0), n = (uint32_t)max(min(hi - kb, 128) - (int)a, 0);
+#pragma unroll
+          for (int k = 0; k < 128; ++k)
+            if ((uint32_t)k - a >= n) sr[k >> 5][k & 31] = 0xff800000u;
+        }
+        auto score = [&](int k) { return __uint_as_float(sr[k >> 5][k & 31]); };
+        // The weights are 2^(s scale - m) for a reference m near the row's maximum so far,
+        // not the maximum itself: any m gives the same quotient, as long as the weights
+        // and their sums stay within fp32 and bf16's common range.  So m is found where
+        // there is none and raised one tile after a weight went beyond 2^8; the hot loop
+        // takes no maximum.
+        if (__any_sync(0xffffffffu, stale)) {
+          float m4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) m4[k] = score(k);
+#pragma unroll
+          for (int k = 4; k < 124; k += 8)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m4[i] = max3(m4[i], score(k + 2 * i), score(k + 2 * i + 1));
+          m4[0] = max3(m4[0], score(124), score(125));
+          m4[1] = max3(m4[1], score(126), score(127));
+          float mx = max3(max3(m4[0], m4[1], m4[2]), m4[3], m4[3]) * p.scale_log2;
+          // a NaN or an infinite maximum: the row is done over in fp32 at the end
+          if (!(mx < CUDART_INF_F)) l = CUDART_NAN_F;
+          // the earlier tiles' largest weight counts as well: l is a bound of it
+          if (l > 1.f) mx = fmaxf(mx, m_used + log2f(l));
+          float alpha = 1.f;
+          bool resc = false;
+          if (mx > m_used) {
+            // (with no weight so far there is nothing to rescale: O holds zeros for this row)
+            alpha = ex2_approx(m_used - mx);
+            resc = l != 0.f;
+            l *= alpha;
+            m_used = mx;
           }
-          tmem_wait_st();
-        }
-        stale = m_used == -CUDART_INF_F;
-      }
-      const float ref = m_used == -CUDART_INF_F ? 0.f : -m_used;
-      const uint64_t ref2 = pack2(ref, ref);
-      uint64_t sum[2] = {0, 0};
-      float top = 0.f;  // the largest exponent that the polynomial was given
-      // the weights of 64 keys, in bf16 pairs over the scores and to the MMA warp; with
-      // `poly` a part of the exponentials goes to the FMA pipe
-      auto weights = [&](int half, auto poly) {
-        uint32_t pk[32];
+          if (__any_sync(0xffffffffu, resc && j > from)) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tl + co + 32u * c, o);
+              tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 32; ++k) {
-          const int u = 64 * half + 2 * k;
-          const uint64_t x = fma2(pack2(score(u), score(u + 1)), scale2, ref2);
-          float p0, p1;
-          if (decltype(poly)::value && ((kPolyPairs >> (k & 7)) & 1)) {
-            unpack2(x, p0, p1);
-            top = max3(top, p0, p1);
-            exp2_poly2(x, p0, p1);
-          } else {
-            unpack2(x, p0, p1);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              tmem_st32(tl + co + 32u * c, o);
+            }
+            tmem_wait_st();
+          }
+          stale = m_used == -CUDART_INF_F;
+        }
+        const float ref = m_used == -CUDART_INF_F ? 0.f : -m_used;
+        const uint64_t ref2 = pack2(ref, ref);
+        uint64_t sum[2] = {0, 0};
+        // the weights of 64 keys, in bf16 pairs over the scores and to the MMA warp
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) {
+            const int u = 64 * half + 2 * k;
+            float p0, p1;
+            unpack2(fma2(pack2(score(u), score(u + 1)), scale2, ref2), p0, p1);
             p0 = ex2_approx(p0);
             p1 = ex2_approx(p1);
+            sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
+            pk[k] = pack_bf16(p0, p1);
           }
-          sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
-          pk[k] = pack_bf16(p0, p1);
+          tmem_st32(tl + cs + 32u * half, pk);
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(bar(B_P + 2 * t + half));
         }
-        tmem_st32(tl + cs + 32u * half, pk);
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_local(bar(B_P + 2 * t + half));
-      };
-      if (masked || __any_sync(0xffffffffu, stale)) {
-        // exact zeros for what is not seen
-        weights(0, Poly<false>());
-        weights(1, Poly<false>());
-      } else {
-        weights(0, Poly<true>());
-        weights(1, Poly<true>());
+        float s0, s1;
+        unpack2(add2(sum[0], sum[1]), s0, s1);
+        const float tile = s0 + s1;
+        l += tile;
+        stale = stale || tile > kRescale;
+        // beyond 2^60 (a NaN included) within one tile: the row is done over as well
+        if (!(tile < kBeyond)) l = CUDART_NAN_F;
       }
-      float s0, s1;
-      unpack2(add2(sum[0], sum[1]), s0, s1);
-      const float tile = s0 + s1;
-      l += tile;
-      stale = stale || tile > kRescale;
-      // beyond 2^60 (a NaN included) within one tile: the row is done over as well
-      if (!(tile < kBeyond && top < 60.f)) l = CUDART_NAN_F;
-    }
-    // ---- o = O / l, lse
-    const bool any = T.to[t] > T.from[t];
-    if (any) {
-      mbar_wait_converged(bar(B_O + t), 0, abort_flag, p.status, wait_ns);
+      // ---- o = O / l, lse
+      ok = ok && wait(B_O + t, nq);
+      ++nq;
+      if (!ok) break;
       tc_fence_after();
-    }
-    const bool live = any && __shfl_sync(0xffffffffu, *abort_flag, 0) == 0;
-    const bool mine = hi > lo;
-    const float inv = l == 0.f || !live ? 0.f : 1.f / l;
-    const int64_t orow = (int64_t)qi * p.H + h;
-    bool odd = live && mine && !(fabsf(l) < CUDART_INF_F);
-#pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
-      uint32_t o[32];
-      if (live) {
-        tmem_ld32(tl + co + 32u * c, o);
-        tmem_wait_ld();
-      } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint32_t o[4][32], pk[64];
+      float bad4[4] = {0.f, 0.f, 0.f, 0.f};  // a NaN once any value is infinite or not a number
 #pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] = 0u;
+      for (int c = 0; c < 4; ++c) tmem_ld32(tl + co + 32u * c, o[c]);
+      tmem_wait_ld();
+      tc_fence_before();
+      arrive(B_READ_O + t);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float x0 = __uint_as_float(o[c][2 * k]), x1 = __uint_as_float(o[c][2 * k + 1]);
+          bad4[k & 3] = fmaf(x0, 0.f, fmaf(x1, 0.f, bad4[k & 3]));
+          pk[16 * c + k] = pack_bf16(x0 * inv, x1 * inv);
+        }
+      const float bad = (bad4[0] + bad4[1]) + (bad4[2] + bad4[3]);
+      const bool mine = hi > lo;
+      const int64_t orow = (int64_t)qi * p.H + h;
+      // Four lanes hold four rows; a store instruction of whole rows would touch 32 lines
+      // of 128 bytes for 32 bytes each.  They exchange 32-byte pieces in two steps, after
+      // which the four write a line of one row together: 8 lines an instruction.
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t* v = pk + 32 * half;  // piece c of this lane's row: v[8 c ..]
+#pragma unroll
+        for (int m = 1; m <= 2; m <<= 1)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (!(c & m))
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const bool up = lane & m;
+                const uint32_t give = up ? v[8 * c + k] : v[8 * (c | m) + k];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, m);
+                if (up)
+                  v[8 * c + k] = got;
+                else
+                  v[8 * (c | m) + k] = got;
+              }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          // piece lane % 4 of the row of lane 4 (lane / 4) + c
+          const int from_lane = (lane & ~3) | c;
+          const bool real = __shfl_sync(0xffffffffu, mine, from_lane);
+          if (real) {
+            __nv_bfloat16* dst = p.out + ((int64_t)(qi - lane + from_lane) * p.H + h) * kDv + 64 * half + 16 * (lane & 3);
+            if (p.wide) {
+              stg256(dst, v + 8 * c);
+            } else {
+              reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[8 * c], v[8 * c + 1], v[8 * c + 2], v[8 * c + 3]);
+              reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[8 * c + 4], v[8 * c + 5], v[8 * c + 6], v[8 * c + 7]);
+            }
+          }
+        }
       }
-      float bad = 0.f;  // a NaN once any value is infinite or not a number
-#pragma unroll
-      for (int k = 0; k < 32; ++k) bad = fmaf(__uint_as_float(o[k]), 0.f, bad);
-      odd = odd || (live && mine && bad != 0.f);
-      if (mine) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + orow * kDv + 32 * c);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          dst[k] = make_uint4(pack_bf16(__uint_as_float(o[8 * k]) * inv, __uint_as_float(o[8 * k + 1]) * inv),
-                              pack_bf16(__uint_as_float(o[8 * k + 2]) * inv, __uint_as_float(o[8 * k + 3]) * inv),
-                              pack_bf16(__uint_as_float(o[8 * k + 4]) * inv, __uint_as_float(o[8 * k + 5]) * inv),
-                              pack_bf16(__uint_as_float(o[8 * k + 6]) * inv, __uint_as_float(o[8 * k + 7]) * inv));
+      if (mine && p.lse) p.lse[orow] = inv == 0.f ? -CUDART_INF_F : (m_used + log2f(l)) * 0.6931471805599453f;
+      // An infinite or NaN value that a row does not see has met its zero weight in the
+      // product with V (0 x inf): such rows, and those that see one, are done over from
+      // the definition.
+      const bool odd = mine && (bad != 0.f || !(fabsf(l) < CUDART_INF_F));
+      __syncwarp();
+      for (uint32_t again = __ballot_sync(0xffffffffu, odd); again; again &= again - 1) {
+        const int r = __ffs(again) - 1;
+        attend_row<PE>(p, __shfl_sync(0xffffffffu, qi, r), h, __shfl_sync(0xffffffffu, lo, r),
+                       __shfl_sync(0xffffffffu, hi, r), lane);
       }
     }
-    if (mine && p.lse) p.lse[orow] = inv == 0.f ? -CUDART_INF_F : (m_used + log2f(l)) * 0.6931471805599453f;
-    // An infinite or NaN value that a row does not see has met its zero weight in the
-    // product with V (0 x inf): such rows, and those that see one, are done over from
-    // the definition.
-    __syncwarp();
-    for (uint32_t again = __ballot_sync(0xffffffffu, odd); again; again &= again - 1) {
-      const int r = __ffs(again) - 1;
-      attend_row<PE>(p, __shfl_sync(0xffffffffu, qi, r), h, __shfl_sync(0xffffffffu, lo, r), __shfl_sync(0xffffffffu, hi, r),
-                     lane);
-    }
-    tc_fence_before();
   }
 
+  tc_fence_before();
   __syncthreads();
-  if (threadIdx.x == 0) {
-    // no load may outlive the block: the queries of a block without keys, and after a
-    // wait that ran out the last round of the ring (all waits bounded)
+  if (*abort_flag && threadIdx.x == 0) {
+    // a wait that ran out may leave loads in flight: wait (bounded) for the last ones
     int give_up = 0;
-    mbar_wait(bar(B_Q), 0, &give_up, nullptr, kDrainNs);
-    for (int i = *abort_flag ? max(0, *issued - 8) : *issued; i < *issued; ++i)
-      mbar_wait(full(i), (i >> 3) & 1, &give_up, nullptr, kDrainNs);
+    for (int i = 0; i < 2; ++i)
+      if (issued[1 + i] > 0) mbar_wait(bar(B_Q + i), (issued[1 + i] - 1) & 1, &give_up, nullptr, kDrainNs);
+    for (int it = max(0, issued[0] - 8); it < issued[0]; ++it)
+      mbar_wait(bar(B_FULL + (it & 7)), (it >> 3) & 1, &give_up, nullptr, kDrainNs);
   }
   __syncthreads();
   if (warp == 1) tmem_dealloc_1(tmem, 512);
@@ -618,6 +769,10 @@ cudaError_t launch_prefill_packed(const mla_prefill_packed_args_t* a, cudaStream
   p.scale_log2 = a->softmax_scale * kLog2e;
   p.blocks = (int)(((int64_t)a->n_tok + kRows - 1) / kRows);
   p.wait_ns = device_wait_limit_ns();
+  p.wide = (reinterpret_cast<uintptr_t>(a->out) & 31u) == 0;  // the ABI asks for 16 bytes
+  const int heads = kHeadGroup * p.share;
+  p.group = heads < a->H ? heads : a->H;
+  p.sorted = p.blocks <= kMaxSorted && (int64_t)p.blocks * a->H > device_sm_count();
   return a->d_r ? launch_tiles<true>(a, p, stream) : launch_tiles<false>(a, p, stream);
 }
 
