@@ -8,12 +8,14 @@
 // operator is bound by reading them, or by latency when few sequences are there.
 //
 // One thread-block cluster per sequence (up to 8 CTAs, so that one sequence draws
-// on 8 SMs' load paths).  The row is cut into segments of 1024 values, one warp
-// each, whose sums all go to the first CTA's shared memory; it finds the segment
-// with a scan over the sums and rescans that segment alone (4 KB, in L2 by then).
-// Sums are fp64: with V near 10^5 values an fp32 sum would move a boundary by
-// more than many a token's probability.  The differences p - q are exact in fp64
-// but for a last bit.  Each sum has one fixed order, so results repeat.
+// on 8 SMs' load paths; fewer when the batch fills the GPU by itself).  The row is
+// cut into segments of 1024 values, a warp each, whose sums all go to the first
+// CTA's shared memory; it finds the segment by a scan over the sums and then reads
+// that segment alone again (4 KB, in L2 by then).  With V near 10^5 values an fp32
+// sum would move a boundary by more than many a token's probability: a lane carries
+// the rounding errors of its differences and sums along (exact to some 2^-45), the
+// sums of segments are fp64.  Each sum has one fixed
+// order, so results repeat.
 #include <math.h>
 
 #include "sm100.cuh"
@@ -47,8 +49,20 @@ MLA_DEVI float ld(const __nv_bfloat16* x, int64_t i) {
   return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(x) + i) << 16);
 }
 
+template <bool kOn>
+struct Is {
+  static constexpr bool value = kOn;
+};
+
 // What a value adds: only what is positive (a NaN is not)
 MLA_DEVI double weight(double w) { return w > 0.0 ? w : 0.0; }
+
+// a + b in fp32 and what its rounding took away (Knuth): together exact
+MLA_DEVI float two_sum(float a, float b, float& low) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  low = __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t));
+  return s;
+}
 
 MLA_DEVI double warp_sum(double x) {
 #pragma unroll
@@ -64,10 +78,26 @@ MLA_DEVI double warp_scan(double x, int lane) {
   return x;
 }
 
+// Of 32 parts in lane order, the first whose running sum (from `run` on) exceeds the
+// goal, else the last that adds anything (rounding may leave the goal unreached);
+// `run` becomes the sum before it.  -1: none adds anything.
+MLA_DEVI int pick(double own, double goal, double& run, int lane) {
+  const double upto = run + warp_scan(own, lane);
+  const uint32_t over = __ballot_sync(0xffffffffu, own > 0.0 && upto > goal);
+  const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
+  if (!some) return -1;
+  const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
+  run = __shfl_sync(0xffffffffu, upto - own, l);
+  return l;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, int cluster) {
-  __shared__ double sums[2][kMaxSegs];  // of the weights, and of p alone
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams p, int cluster) {
+  __shared__ double sums[2][kMaxSegs];  // of what is left of p, and of p where nothing is left
+  __shared__ double parts[32];          // of one segment
   __shared__ int first_bad[2];          // first rejected draft; whether an argument is bad
+  __shared__ int found[2];              // the segment of the next token (-1: none), the row of sums it came from
+  // No early trigger: new_lens may be the lengths that a decode reads before it waits.
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster > 1 ? sm100::cluster_ctarank() : 0;
@@ -101,29 +131,53 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     const T* qr = a < n && Q ? Q + a * p.q_row : nullptr;
     const int certain = a < n && !Q ? p.draft[(int64_t)b * most + a] : -1;  // draft of probability one
     const int segs = (p.V + kSeg - 1) / kSeg;
-    // a value's two weights: what is left of p, and p
-    auto at = [&](int j, double& left, double& whole) {
-      const double pv = (double)ld(pr, j);
-      whole = weight(pv);
-      left = qr ? weight(pv - (double)ld(qr, j)) : j == certain ? weight(pv - 1.0) : whole;
-    };
+    constexpr int kN = 16;
     for (int g = warp * cluster + rank; g < segs; g += kWarps * cluster) {
-      double sl = 0.0, sw = 0.0;
-#pragma unroll 8
-      for (int k = 0; k < kSeg / 32; ++k) {
-        const int j = g * kSeg + 32 * k + lane;
-        if (j < p.V) {
-          double left, whole;
-          at(j, left, whole);
-          sl += left;
-          sw += whole;
+      const int j0 = g * kSeg + lane;
+      const bool inside = (g + 1) * kSeg <= p.V;
+      float acc = 0.f, low = 0.f;
+      // kN values of each row, the loads of all of them without a branch between them, so
+      // that they are on their way together
+      auto add = [&](int j, auto whole, auto two) {
+        float pv[kN], qv[kN];
+#pragma unroll
+        for (int k = 0; k < kN; ++k) pv[k] = ld(pr, decltype(whole)::value ? j + 32 * k : min(j + 32 * k, p.V - 1));
+#pragma unroll
+        for (int k = 0; k < kN; ++k)
+          qv[k] = !decltype(two)::value ? (j + 32 * k == certain ? 1.f : 0.f)
+                                        : ld(qr, decltype(whole)::value ? j + 32 * k : min(j + 32 * k, p.V - 1));
+#pragma unroll
+        for (int k = 0; k < kN; ++k) {
+          // p - min(q, p) is zero or positive, and what rounding took from it comes out
+          // exactly since p >= q (Dekker); then the running sum with its rounding error
+          const float x = decltype(whole)::value || j + 32 * k < p.V ? fmaxf(pv[k], 0.f) : 0.f, y = fminf(qv[k], x);
+          const float d = __fsub_rn(x, y), e = __fsub_rn(__fsub_rn(x, d), y);
+          float f;
+          acc = two_sum(acc, d, f);
+          low += e + f;
         }
+      };
+#pragma unroll 1
+      for (int j = j0; j < j0 + kSeg; j += 32 * kN) {
+        if (inside && qr)
+          add(j, Is<true>(), Is<true>());
+        else if (inside)
+          add(j, Is<true>(), Is<false>());
+        else if (qr)
+          add(j, Is<false>(), Is<true>());
+        else
+          add(j, Is<false>(), Is<false>());
       }
-      sl = warp_sum(sl);
-      sw = warp_sum(sw);
+      const double sum = warp_sum((double)acc + (double)low);
+      // where nothing is left of the target, its own sum, in case nothing is left anywhere
+      double whole = 0.0;
+      if (sum == 0.0) {
+        for (int k = 0; k < kSeg / 32; ++k) whole += weight((double)ld(pr, min(j0 + 32 * k, p.V - 1)) * (j0 + 32 * k < p.V ? 1.0 : 0.0));
+        whole = warp_sum(whole);
+      }
       if (lane < 2) {
         const uint32_t here = smem_u32(&sums[lane][g]);
-        const double v = lane ? sw : sl;
+        const double v = lane ? whole : sum;
         if (cluster > 1)
           asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(sm100::mapa(here, 0)), "d"(v) : "memory");
         else
@@ -136,62 +190,57 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const VerifyParams p, 
     } else {
       __syncthreads();
     }
-    if (rank != 0 || warp != 0) return;
-    // the total is the last running sum, so that u * total stays below it
-    int row = 0;
-    double total = 0.0;
-    auto total_of = [&](int r) {
-      double run = 0.0;
-      for (int g0 = 0; g0 < segs; g0 += 32) {
-        const double x = warp_scan(g0 + lane < segs ? sums[r][g0 + lane] : 0.0, lane);
-        run += __shfl_sync(0xffffffffu, x, 31);
+    if (rank != 0) return;
+    double goal = 0.0, run = 0.0;
+    if (warp == 0) {
+      // a lane has `per` neighbouring segments
+      const int per = (segs + 31) / 32, s0 = min(lane * per, segs), s1 = min(s0 + per, segs);
+      auto own_of = [&](int row) {
+        double x = 0.0;
+        for (int g = s0; g < s1; ++g) x += sums[row][g];
+        return x;
+      };
+      int row = 0, seg = -1;
+      double own = own_of(0);
+      double total = __shfl_sync(0xffffffffu, warp_scan(own, lane), 31);
+      if (total == 0.0 && a < n) {
+        row = 1;
+        own = own_of(1);
+        total = __shfl_sync(0xffffffffu, warp_scan(own, lane), 31);
       }
-      return run;
+      if (total > 0.0 && total < INFINITY) {
+        goal = (double)p.u_sample[b] * total;
+        const int l = pick(own, goal, run, lane);
+        const int first = __shfl_sync(0xffffffffu, s0, l), many = __shfl_sync(0xffffffffu, s1, l) - first;
+        seg = first + pick(lane < many ? sums[row][first + lane] : 0.0, goal, run, lane);
+      }
+      if (lane == 0) {
+        found[0] = seg;
+        found[1] = row;
+      }
+    }
+    __syncthreads();
+    const int seg = found[0], row = found[1];
+    // the segment's values again, 128 to a warp, in 32 parts of 32
+    auto value = [&](int j) {
+      const float pv = ld(pr, min(j, p.V - 1)), qv = qr ? ld(qr, min(j, p.V - 1)) : j == certain ? 1.f : 0.f;
+      return j < p.V ? weight((double)pv - (row ? 0.0 : (double)qv)) : 0.0;
     };
-    total = total_of(0);
-    if (!(total > 0.0) && a < n) total = total_of(row = 1);
-    if (total > 0.0 && total < INFINITY) {
-      const double goal = (double)p.u_sample[b] * total;
-      // the first segment whose running sum exceeds the goal (else the last that adds anything)
-      double run = 0.0, base = 0.0;
-      int seg = -1, last = -1;
-      double last_base = 0.0;
-      for (int g0 = 0; g0 < segs && seg < 0; g0 += 32) {
-        const double own = g0 + lane < segs ? sums[row][g0 + lane] : 0.0;
-        const double x = run + warp_scan(own, lane);
-        const uint32_t over = __ballot_sync(0xffffffffu, own > 0.0 && x > goal);
-        const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
-        if (over) {
-          const int l = __ffs(over) - 1;
-          seg = g0 + l;
-          base = __shfl_sync(0xffffffffu, x - own, l);
-        } else if (some) {
-          const int l = 31 - __clz(some);
-          last = g0 + l;
-          last_base = __shfl_sync(0xffffffffu, x - own, l);
-        }
-        run = __shfl_sync(0xffffffffu, x, 31);
+    if (seg >= 0) {
+      double x[kSeg / 32 / kWarps];
+#pragma unroll
+      for (int k = 0; k < kSeg / 32 / kWarps; ++k) x[k] = value(seg * kSeg + 128 * warp + 32 * k + lane);
+#pragma unroll
+      for (int k = 0; k < kSeg / 32 / kWarps; ++k) {
+        x[k] = warp_sum(x[k]);
+        if (lane == 0) parts[warp * (kSeg / 32 / kWarps) + k] = x[k];
       }
-      if (seg < 0) {
-        seg = last;
-        base = last_base;
-      }
-      run = base;
-      for (int k = 0; k < kSeg / 32; ++k) {
-        const int j = seg * kSeg + 32 * k + lane;
-        double left = 0.0, whole = 0.0;
-        if (j < p.V) at(j, left, whole);
-        const double own = row ? whole : left;
-        const double x = run + warp_scan(own, lane);
-        const uint32_t over = __ballot_sync(0xffffffffu, own > 0.0 && x > goal);
-        const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
-        if (over) {
-          next = seg * kSeg + 32 * k + __ffs(over) - 1;
-          break;
-        }
-        if (some) next = seg * kSeg + 32 * k + 31 - __clz(some);  // stands if rounding leaves the goal unreached
-        run = __shfl_sync(0xffffffffu, x, 31);
-      }
+    }
+    __syncthreads();
+    if (warp != 0) return;
+    if (seg >= 0) {
+      const int j = seg * kSeg + 32 * pick(parts[lane], goal, run, lane);
+      next = j + pick(value(j + lane), goal, run, lane);
     }
   } else if (rank != 0 || warp != 0) {
     return;
@@ -228,10 +277,10 @@ cudaError_t launch_verify(const mla_verify_args_t* a, cudaStream_t stream) {
   p.q_row = a->draft_row;
   p.s_q = a->s_q;
   p.V = a->V;
-  // one segment per warp, up to 8 CTAs
+  // a segment per warp, up to 8 CTAs, but no more than about eight CTAs an SM in all (four are resident)
   const int segs = (a->V + kSeg - 1) / kSeg;
   int cluster = 1;
-  while (cluster < 8 && cluster * kWarps < segs) cluster *= 2;
+  while (cluster < 8 && cluster * kWarps < segs && 2ll * cluster * a->B <= 8ll * device_sm_count()) cluster *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a->B * cluster);
   cfg.blockDim = dim3(kThreads);
