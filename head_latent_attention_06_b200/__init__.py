@@ -797,7 +797,12 @@ def mla_verify_draft(args: VerifyArgs, stream=None):
 
 def mla_get_status(workspace, stream=None) -> int:
     """Waits for the stream and returns (and clears) the device status word."""
-    return int(load().mla_get_status(_ptr(workspace), _stream(stream)))
+    import torch
+    dev = getattr(workspace, "device", None)
+    if dev is None or dev.type != "cuda" or dev.index == torch.cuda.current_device():
+        return int(load().mla_get_status(_ptr(workspace), _stream(stream)))
+    with torch.cuda.device(dev):
+        return int(load().mla_get_status(_ptr(workspace), _stream(stream)))
 
 
 def mla_status_string(code: int) -> str:

@@ -166,7 +166,7 @@ mla_status_t check_stride(int64_t s, int64_t extent) {
 mla_status_t check_append_shape(const mla_append_args_t* a) {
   if (!a) return MLA_ERR_INVALID_VALUE;
   if (a->B < 0 || a->H < 0 || a->n_tok < 0 || a->num_pages < 0 || a->max_pages_per_seq <= 0) return MLA_ERR_INVALID_VALUE;
-  if (a->n_tok > kMaxPacked || a->H > 128) return MLA_ERR_UNSUPPORTED;
+  if (a->n_tok > kMaxPacked || a->B > kMaxPacked || a->H > 128) return MLA_ERR_UNSUPPORTED;
   if (a->d_c != kDc || a->d_r != kDr || a->page_size != kPage) return MLA_ERR_UNSUPPORTED;
   if (a->max_pages_per_seq > 0x7fffffff / kPage) return MLA_ERR_UNSUPPORTED;
   if (a->kv_dtype != MLA_KV_BF16 && a->kv_dtype != MLA_KV_FP8_E4M3 && a->kv_dtype != MLA_KV_Q8_0 &&
@@ -180,7 +180,7 @@ mla_status_t check_packed_shape(const mla_prefill_packed_args_t* a) {
   if (!a) return MLA_ERR_INVALID_VALUE;
   if (a->B < 0 || a->H <= 0 || a->H_kv <= 0 || a->n_tok < 0) return MLA_ERR_INVALID_VALUE;
   if (a->d_n != kDn || a->d_v != kDv || (a->d_r != kDr && a->d_r != 0)) return MLA_ERR_UNSUPPORTED;
-  if (a->H > 128 || a->n_tok > kMaxPacked) return MLA_ERR_UNSUPPORTED;
+  if (a->H > 128 || a->n_tok > kMaxPacked || a->B > kMaxPacked) return MLA_ERR_UNSUPPORTED;
   if (a->H % a->H_kv) return MLA_ERR_INVALID_VALUE;
   if (!(a->softmax_scale > 0.f) || !isfinite(a->softmax_scale)) return MLA_ERR_INVALID_VALUE;
   return MLA_OK;

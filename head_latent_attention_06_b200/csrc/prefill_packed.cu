@@ -8,6 +8,10 @@
 
 namespace mla {
 uint64_t device_wait_limit_ns();
+// tma_map_3d without the cache of encoded maps, for tensors that a caller passes anew
+// each time (tma_host.cu)
+bool tma_map_3d_fresh(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1, uint64_t s2,
+                      uint32_t b0, uint32_t b1, uint32_t b2);
 
 namespace {
 
@@ -161,6 +165,51 @@ MLA_DEVI uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+// Four single-CTA MMAs of one chunk (K = 64 in steps of 16) in one go: one election
+// and one set of operands for the four, descriptors advanced by the given steps (in
+// their 16-byte units; tensor-memory A by columns).  `accumulate` is the first one's;
+// the others always accumulate.
+template <int kAStep, int kBStep>
+MLA_DEVI void mma_1_x4_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 rx;\n\t.reg .b64 a, b;\n\t"
+      "elect.sync rx|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep)
+      : "memory");
+}
+template <int kAStep, int kBStep>
+MLA_DEVI void mma_1_ts_x4_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 rx, a;\n\t.reg .b64 b;\n\t"
+      "elect.sync rx|e, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.eq.b32 q, 0, 0;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.s32 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.s32 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.s32 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep)
+      : "memory");
+}
+// Moves a warpgroup's share of the register file: the sum over the block's
+// warpgroups must not exceed what the block was launched with.
+template <int kRegs>
+MLA_DEVI void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <int kRegs>
+MLA_DEVI void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+
 // The next block that has not been started, asked of the launch control: written to
 // `answer` (16 bytes, counted on `bar`), read by next_block (negative: there is none).
 MLA_DEVI void ask_next(uint32_t answer, uint32_t bar) {

@@ -421,51 +421,6 @@ MLA_DEVI void mma_1_ts_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, u
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Four single-CTA MMAs of one chunk (K = 64 in steps of 16) in one go: one election
-// and one set of operands for the four, descriptors advanced by the given steps (in
-// their 16-byte units; tensor-memory A by columns).  `accumulate` is the first one's;
-// the others always accumulate.
-template <int kAStep, int kBStep>
-MLA_DEVI void mma_1_x4_elect(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 rx;\n\t.reg .b64 a, b;\n\t"
-      "elect.sync rx|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.eq.b32 q, 0, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
-      "add.s64 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
-      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
-      "add.s64 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep)
-      : "memory");
-}
-template <int kAStep, int kBStep>
-MLA_DEVI void mma_1_ts_x4_elect(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q, e;\n\t.reg .b32 rx, a;\n\t.reg .b64 b;\n\t"
-      "elect.sync rx|e, 0xffffffff;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.eq.b32 q, 0, 0;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
-      "add.s32 a, %1, %5;\n\tadd.s64 b, %2, %6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
-      "add.s32 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
-      "add.s32 a, a, %5;\n\tadd.s64 b, b, %6;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "n"(kAStep), "n"(kBStep)
-      : "memory");
-}
-// Moves a warpgroup's share of the register file: the sum over the block's
-// warpgroups must not exceed what the block was launched with.
-template <int kRegs>
-MLA_DEVI void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-template <int kRegs>
-MLA_DEVI void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
-
 // Arrive once on a barrier of this CTA when every tcgen05 operation this thread
 // issued before has completed.
 MLA_DEVI void commit_1_elect(uint32_t bar) {

@@ -17,10 +17,6 @@ bool tma_map_2d(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, u
 bool tma_map_3d(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
                 uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
 
-// tma_map_3d without the cache, for tensors that a caller passes anew each time.
-bool tma_map_3d_fresh(CUtensorMap* m, const void* ptr, uint64_t d0, uint64_t d1, uint64_t d2, uint64_t s1,
-                      uint64_t s2, uint32_t b0, uint32_t b1, uint32_t b2);
-
 // Map of rank 1..5: dims[i] values along dimension i (dimension 0 contiguous),
 // strides[i] the byte stride of dimension i + 1 (any order, multiples of 16),
 // boxes of box[i] values.  The box lands in shared memory with dimension 0

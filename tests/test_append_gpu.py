@@ -255,3 +255,28 @@ def test_append_on_another_stream_and_in_a_graph(cuda_lib):
     check(dict(x, lens=x["lens"] - 1), dict(cache=d["cache"].cpu(), scale=d["scale"].cpu(), k=k_out.cpu(), q=q_out.cpu()))
 
 
+
+
+@pytest.mark.parametrize("kv", ["bf16", "q4_0"])
+def test_append_far_pages(cuda_lib, kv):
+    """Rows more than 2^32 bytes into the cache."""
+    P = 60000 if kv == "bf16" else 250000
+    x = make([3, 2], [66, 64], 16, kv, seed=12)
+    small = x["cache"].shape[0]
+    cache = torch.zeros(P, *x["cache"].shape[1:], dtype=x["cache"].dtype, device="cuda")
+    scale = None if x["scale"] is None else torch.zeros(P, 64, 18, dtype=torch.float16, device="cuda")
+    shift = P - small
+    d = {k: v.cuda() for k, v in x.items() if torch.is_tensor(v)}
+    k_out, q_out = torch.zeros(5, 64, dtype=bf16, device="cuda"), torch.zeros(5, 16, 64, dtype=bf16, device="cuda")
+    cache[shift:] = d["cache"]
+    if scale is not None:
+        scale[shift:] = d["scale"]
+    table = d["table"] + shift
+    a = cuda_lib.make_append_args(c=d["joint"][:, :512], k_pe=d["joint"][:, 512:576], q_pe=d["q"], k_pe_out=k_out,
+                                  q_pe_out=q_out, kv_cache=cache, kv_scale=scale, block_table=table,
+                                  cu_seqlens=d["cu"], seq_lens=d["lens"])
+    ws = cuda_lib.alloc_workspace(a)
+    cuda_lib.mla_append_kv(a)
+    assert cuda_lib.mla_get_status(ws) == 0
+    check(x, dict(cache=cache[shift:].cpu(), scale=None if scale is None else scale[shift:].cpu(), k=k_out.cpu(), q=q_out.cpu()))
+    assert not bool(cache[:shift].view(torch.uint8).any())

@@ -117,34 +117,126 @@ def test_packed_matches_oracle(cuda_lib, lens, H, H_kv, d_r, kw, causal):
 
 def test_packed_long_sampled(cuda_lib):
     """A long prompt between short ones: sampled rows against the definition."""
-    lens = [5, 5000, 300]
-    x = make(lens, 4, 2, 64, seed=3)
+    x = make([5, 5000, 300], 4, 2, 64, seed=3)
     assert run(cuda_lib, x) == 0
-    q = torch.cat([x["q_nope"], x["q_pe"]], -1).cpu()
-    k = torch.cat([x["k_nope"], x["k_pe"][:, None].expand(-1, 2, -1)], -1).cpu()
-    v, rows = x["v"].cpu(), [4, 5, 132, 133, 1000, 2600, 4999, 5004, 5005, 5304]
-    n = sum(lens)
-    o, lse = np.full((n, 4, 128), np.nan), np.full((n, 4), np.nan)
-    mass, size = o.copy(), lse.copy()
-    cu = [0, 5, 5005, 5305]
-    for t in rows:
-        lo = max(c for c in cu if c <= t)
-        got = one_row(q[t], k[lo:t + 1], v[lo:t + 1])
-        o[t], lse[t], mass[t], size[t] = (a[-1] for a in got)
-    check(x, (o, lse, mass, size))
+    check_rows(x, [4, 5, 132, 133, 1000, 2600, 4999, 5004, 5005, 5304])
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_packed_more_blocks_than_the_gpu_holds(cuda_lib, causal):
+    """Blocks in order of their work, several to an SM, an odd number of heads."""
+    x = make([500, 3, 0, 130, 256, 340], 41, 41, 64, seed=11, tail=2)
+    assert run(cuda_lib, x, causal) == 0
+    check(x, oracle_of(x, causal))
+    untouched(x)
+
+
+def test_packed_more_rows_than_are_sorted(cuda_lib):
+    """More than 128 blocks of rows: taken from the end on."""
+    x = make([20000, 13800, 1, 700], 4, 1, 0, seed=12)
+    assert run(cuda_lib, x) == 0
+    check_rows(x, [0, 127, 4097, 12345, 19999, 20000, 20128, 33799, 33800, 33801, 34500])
+
+
+def test_packed_offsets_beyond_32_bits(cuda_lib):
+    """More than 2^31 query and output values."""
+    n, H = 132000, 128                       # 2.16e9 values each
+    lens = [250] * (n // 250)
+    q = torch.zeros(n, H, 128, dtype=bf16, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(13)
+    q[-250:] = torch.randn(250, H, 128, generator=g, device="cuda").to(bf16)
+    k, v = (torch.randn(n, 1, 128, generator=g, device="cuda").to(bf16) for _ in range(2))
+    x = dict(q_nope=q, q_pe=None, k_nope=k, k_pe=None, v=v, cu_seqlens=torch.tensor([0] + list(np.cumsum(lens)), dtype=i32).cuda(),
+             out=torch.empty(n, H, 128, dtype=bf16, device="cuda"), lse=torch.empty(n, H, device="cuda"))
+    assert run(cuda_lib, x) == 0
+    check_rows(x, [250, 131071, n - 250, n - 1])
+
+
+def test_packed_scores_that_keep_rising(cuda_lib):
+    """Scores that rise along the prompt by less than, about and far more than the range
+    that the running reference leaves open, and one that falls."""
+    for steps in (0.02, 0.2, 2.0, -0.2):
+        x = make([700], 2, 1, 0, seed=14)
+        x["q_nope"].zero_()
+        x["k_nope"].zero_()
+        x["q_nope"][:, :, 0] = 128 ** 0.5                       # the score is k's first value
+        x["k_nope"][:, 0, 0] = (torch.arange(700, device="cuda") * steps).to(bf16)
+        assert run(cuda_lib, x) == 0
+        check(x, oracle_of(x, True))
+    # one key far above all before it, and a far higher one in the same tile
+    x["k_nope"].zero_()
+    x["k_nope"][300, 0, 0] = 90.0
+    x["k_nope"][333, 0, 0] = 1000.0
+    x["k_nope"][650, 0, 0] = 1100.0
+    assert run(cuda_lib, x) == 0
+    check(x, oracle_of(x, True))
+
+
+def test_packed_nothing_to_do(cuda_lib):
+    """Rows, but no sequence with any."""
+    x = make([0, 0, 0], 4, 4, 64, seed=15, tail=300)
+    assert run(cuda_lib, x) == 0
+    untouched(x)
+
+
+def test_packed_wait_that_runs_out(cuda_lib):
+    """At a limit of 1 ns the kernel gives up, says so and leaves the context usable."""
+    x = make([300, 100], 16, 16, 64, seed=16)
+    cuda_lib.mla_set_device_wait_limit(1)
+    try:
+        assert run(cuda_lib, x) == 6
+    finally:
+        cuda_lib.mla_set_device_wait_limit(0)
+    assert run(cuda_lib, x) == 0
+    check(x, oracle_of(x, True))
+
+
+def test_packed_two_streams_at_once(cuda_lib):
+    """Calls that overlap share nothing."""
+    xs = [make([400, 300], 32, 32, 64, seed=17 + i) for i in range(2)]
+    args = [cuda_lib.make_prefill_packed_args(**x, causal=True, softmax_scale=1 / 192 ** 0.5) for x in xs]
+    ws = cuda_lib.alloc_workspace(args[0])
+    args[1].workspace, args[1].workspace_bytes = args[0].workspace, args[0].workspace_bytes
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for a, s in zip(args, streams):
+            cuda_lib.mla_prefill_packed(a, s)
+    torch.cuda.synchronize()
+    assert cuda_lib.mla_get_status(ws) == 0
+    for x in xs:
+        first, lse = x["out"].clone(), x["lse"].clone()
+        x["out"].fill_(7)
+        assert run(cuda_lib, x) == 0
+        assert torch.equal(first, x["out"]) and torch.equal(lse, x["lse"])
 
 
 def one_row(q, k, v):
-    """The last row of a causal prompt."""
+    """The last row of a causal prompt: q [H][d], k and v [keys][H_kv][..]."""
     q, k, v = f64(q), f64(k), f64(v)
+    share, scale = q.shape[0] // k.shape[1], q.shape[1] ** -0.5
     out = []
     for h in range(q.shape[0]):
-        kk, vv = k[:, h // 2], v[:, h // 2]
-        s = kk @ q[h] / 192 ** 0.5
+        kk, vv = k[:, h // share], v[:, h // share]
+        s = kk @ q[h] * scale
         p = np.exp(s - s.max())
         out.append(((p / p.sum()) @ vv, s.max() + np.log(p.sum()), (p / p.sum()) @ np.abs(vv),
-                    (np.abs(kk) @ np.abs(q[h])).max() / 192 ** 0.5))
+                    (np.abs(kk) @ np.abs(q[h])).max() * scale))
     return [np.stack([o[i] for o in out])[None] for i in range(4)]
+
+
+def check_rows(x, rows):
+    """These rows of a causal batch against the definition."""
+    cu = x["cu_seqlens"].tolist()
+    for t in rows:
+        lo = max(c for c in cu if c <= t)
+        q, k = x["q_nope"][t], x["k_nope"][lo:t + 1]
+        if x["q_pe"] is not None:
+            q = torch.cat([q, x["q_pe"][t]], -1)
+            k = torch.cat([k, x["k_pe"][lo:t + 1, None].expand(-1, k.shape[1], -1)], -1)
+        o, lse, mass, size = one_row(q, k, x["v"][lo:t + 1])
+        part = dict(out=x["out"][t:t + 1], lse=x["lse"][t:t + 1])
+        check(part, (o, lse, mass, size))
 
 
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])

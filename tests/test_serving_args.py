@@ -69,7 +69,7 @@ REFUSED = [
         (dict(B=-1), INVALID), (dict(H=-1), INVALID), (dict(n_tok=-1), INVALID), (dict(num_pages=-1), INVALID),
         (dict(max_pages_per_seq=0), INVALID), (dict(H=129), UNSUPPORTED), (dict(d_c=256), UNSUPPORTED),
         (dict(d_r=32), UNSUPPORTED), (dict(page_size=16), UNSUPPORTED), (dict(kv_dtype=4), UNSUPPORTED),
-        (dict(n_tok=(1 << 30) + 1), UNSUPPORTED), (dict(max_pages_per_seq=1 << 26), UNSUPPORTED),
+        (dict(n_tok=(1 << 30) + 1), UNSUPPORTED), (dict(B=(1 << 30) + 1), UNSUPPORTED), (dict(max_pages_per_seq=1 << 26), UNSUPPORTED),
         (dict(rope_base=0.0), INVALID), (dict(rope_base=float("inf")), INVALID), (dict(rope_base=float("nan")), INVALID),
         (dict(workspace=None), INVALID), (dict(workspace=P + 8), MISALIGNED), (dict(workspace_bytes=255), WS_SMALL),
         (dict(c=None), INVALID), (dict(k_pe=None), INVALID), (dict(q_pe=None), INVALID), (dict(q_pe_out=None), INVALID),
@@ -84,7 +84,7 @@ REFUSED = [
     (packed_args, "mla_prefill_packed", [
         (dict(B=-1), INVALID), (dict(H=0), INVALID), (dict(H_kv=0), INVALID), (dict(n_tok=-1), INVALID),
         (dict(H_kv=3), INVALID), (dict(H_kv=32), INVALID), (dict(H=256), UNSUPPORTED), (dict(d_n=64), UNSUPPORTED),
-        (dict(d_r=32), UNSUPPORTED), (dict(d_v=64), UNSUPPORTED), (dict(n_tok=(1 << 30) + 1), UNSUPPORTED),
+        (dict(d_r=32), UNSUPPORTED), (dict(d_v=64), UNSUPPORTED), (dict(n_tok=(1 << 30) + 1), UNSUPPORTED), (dict(B=(1 << 30) + 1), UNSUPPORTED),
         (dict(softmax_scale=0.0), INVALID), (dict(softmax_scale=-1.0), INVALID), (dict(softmax_scale=float("nan")), INVALID),
         (dict(softmax_scale=float("inf")), INVALID),
         (dict(workspace=None), INVALID), (dict(workspace=P + 4), MISALIGNED), (dict(workspace_bytes=0), WS_SMALL),
@@ -191,6 +191,40 @@ def test_builders_reject_bad_tensors(which, field, bad, msg):
     t[field] = bad
     with pytest.raises(ValueError, match=msg):
         build(**t, **kw)
+
+
+def test_entry_points_make_the_tensors_device_current(monkeypatch):
+    """Arguments on another device than the current one: the call is made with theirs
+    current and on that device's stream."""
+    seen = []
+    current = [0]
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.dev.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    class Lib:
+        def mla_append_kv(self, args, stream):
+            seen.append((current[0], stream))
+            return 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(mla, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(mla, "_lib", Lib())
+    a = append_args()
+    for index in (0, 1):
+        a.device = torch.device("cuda", index)
+        mla.mla_append_kv(a)
+    a.device = torch.device("cuda", 1)
+    mla.mla_append_kv(a, stream=7)
+    assert seen == [(0, 100), (1, 101), (1, 7)] and current[0] == 0
 
 
 # ------------------------------------------------------------------ the oracle's own pins

@@ -61,7 +61,7 @@ def check(got, want):
 @pytest.mark.parametrize("B,S,V,ragged", [
     (1, 0, 1, False), (1, 1, 2, False), (3, 2, 7, True), (5, 4, 31, True), (2, 3, 1000, False), (4, 3, 1024, True),
     (4, 3, 1025, True), (3, 5, 8191, True), (2, 2, 8193, False), (9, 4, 32000, True), (3, 7, 100003, True),
-    (2, 1, 1 << 20, False), (130, 3, 2049, True), (2, 1023, 65, True), (40, 8, 16, True),
+    (2, 1, 1 << 20, False), (130, 3, 2049, True), (2, 1023, 65, True), (40, 8, 16, True), (700, 2, 3000, True), (300, 1, 9000, False),
 ])
 def test_verify_matches_oracle(cuda_lib, B, S, V, ragged, dtype):
     x = make(B, S, V, dtype, seed=B + S + V, ragged=ragged)
@@ -122,6 +122,36 @@ def test_verify_edges(cuda_lib):
     check(run(cuda_lib, x), want)
     assert want[1][2] == 2 and want[1][3] == 0 and want[0][7, 0] == -1
     assert V // 2 <= want[0][4, 0] < V // 2 + 5
+
+
+def test_verify_truncated_distributions(cuda_lib):
+    """Only a few tokens have any probability (a cut to the likeliest): whole segments
+    of zeros, drafts outside the target's set, sets that are the same."""
+    x = make(12, 3, 20000, seed=9, ragged=True)
+    for name, cut in (("target_probs", 40), ("draft_probs", 60)):
+        t = x[name]
+        low = t.topk(cut, -1).values[..., -1:]
+        t[t < low] = 0.0
+        t /= t.sum(-1, keepdim=True)
+    x["draft_probs"][:4] = x["target_probs"][:4, :3]
+    x["u_accept"][:4] = 1 - 2.0 ** -24
+    g = torch.Generator().manual_seed(10)
+    x["draft_tokens"] = torch.stack([torch.multinomial(q, 1, generator=g)[:, 0] for q in x["draft_probs"]]).to(i32)
+    check(run(cuda_lib, x), oracle_of(x))
+
+
+def test_verify_close_boundaries(cuda_lib):
+    """u_sample a hair on either side of a running sum: what 32-bit sums would miss."""
+    V = 60000
+    x = make(2, 0, V, seed=11, sharp=0.5)
+    p = x["target_probs"][:, 0].double().numpy()
+    sums = np.cumsum(p, -1)
+    j = 41234
+    for b, eps in ((0, 1e-6), (1, -1e-6)):
+        edge = (sums[b, j] + eps * p[b, j]) / sums[b, -1]
+        u = np.float32(edge)
+        x["u_sample"][b] = float(u)
+    check(run(cuda_lib, x), oracle_of(x))
 
 
 def test_verify_not_a_number(cuda_lib):
