@@ -13,6 +13,12 @@
 // pairs) whose place in the vector is the same for all of its pieces, so the
 // eight shuffles are done once a warp.  The angle is a fraction of a turn in fp64
 // (positions beyond 10^5 turn thousands of times), its sine and cosine fp32.
+//
+// A warp has up to 32 heads (8 pieces of 16 bytes a lane, four in flight at a time);
+// more heads take two or four warps a token, each with its own sincos, which are free
+// beside the loads.  Measured: 16351 tokens, 128 heads, e4m3 cache 101 us = 5.6 TB/s, 0.85
+// of the copy rate; one step of 64 tokens, 128 heads, bf16 cache 3.4 us in a CUDA graph
+// (0.34 us of bytes: launch and three dependent reads - offsets, length, page).
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>

@@ -16,6 +16,12 @@
 // the rounding errors of its differences and sums along (exact to some 2^-45), the
 // sums of segments are fp64.  Each sum has one fixed
 // order, so results repeat.
+//
+// Measured: 256 sequences, 3 drafts, 128000 fp32 values 46 us = 4.8 TB/s (0.73 of the
+// copy rate; sequences whose drafts were all accepted read one row, the others two, and
+// the search at the end is not hidden); 33 sequences, 100003 bf16 values 9 us; one
+// sequence, 32000 values 6.1 us in a CUDA graph, of which 2 us are the dependent reads of
+// draft, probabilities and row and 2.5 us the search.
 #include <math.h>
 
 #include "sm100.cuh"
