@@ -87,14 +87,17 @@ MLA_DEVI double warp_scan(double x, int lane) {
 // Of 32 parts in lane order, the first whose running sum (from `run` on) exceeds the
 // goal, else the last that adds anything (rounding may leave the goal unreached);
 // `run` becomes the sum before it.  -1: none adds anything.
-MLA_DEVI int pick(double own, double goal, double& run, int lane) {
-  const double upto = run + warp_scan(own, lane);
+// `upto`: the running sums, this part's included.
+MLA_DEVI int pick_of(double own, double upto, double goal, double& run) {
   const uint32_t over = __ballot_sync(0xffffffffu, own > 0.0 && upto > goal);
   const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
   if (!some) return -1;
   const int l = over ? __ffs(over) - 1 : 31 - __clz(some);
   run = __shfl_sync(0xffffffffu, upto - own, l);
   return l;
+}
+MLA_DEVI int pick(double own, double goal, double& run, int lane) {
+  return pick_of(own, run + warp_scan(own, lane), goal, run);
 }
 
 template <typename T>
@@ -207,18 +210,20 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
         return x;
       };
       int row = 0, seg = -1;
-      double own = own_of(0);
-      double total = __shfl_sync(0xffffffffu, warp_scan(own, lane), 31);
+      double own = own_of(0), upto = warp_scan(own, lane);
+      double total = __shfl_sync(0xffffffffu, upto, 31);
       if (total == 0.0 && a < n) {
         row = 1;
         own = own_of(1);
-        total = __shfl_sync(0xffffffffu, warp_scan(own, lane), 31);
+        upto = warp_scan(own, lane);
+        total = __shfl_sync(0xffffffffu, upto, 31);
       }
       if (total > 0.0 && total < INFINITY) {
         goal = (double)p.u_sample[b] * total;
-        const int l = pick(own, goal, run, lane);
-        const int first = __shfl_sync(0xffffffffu, s0, l), many = __shfl_sync(0xffffffffu, s1, l) - first;
-        seg = first + pick(lane < many ? sums[row][first + lane] : 0.0, goal, run, lane);
+        const int l = pick_of(own, upto, goal, run);
+        seg = __shfl_sync(0xffffffffu, s0, l);
+        const int many = __shfl_sync(0xffffffffu, s1, l) - seg;
+        if (per > 1) seg += pick(lane < many ? sums[row][seg + lane] : 0.0, goal, run, lane);
       }
       if (lane == 0) {
         found[0] = seg;
