@@ -17,8 +17,10 @@
 // A warp has up to 32 heads (8 pieces of 16 bytes a lane, four in flight at a time);
 // more heads take two or four warps a token, each with its own sincos, which are free
 // beside the loads.  Measured: 16351 tokens, 128 heads, e4m3 cache 101 us = 5.6 TB/s, 0.85
-// of the copy rate; one step of 64 tokens, 128 heads, bf16 cache 3.4 us in a CUDA graph
-// (0.34 us of bytes: launch and three dependent reads - offsets, length, page).
+// of the copy rate; one step of 64 tokens, 128 heads, bf16 cache 2.8 us in a CUDA graph
+// (0.34 us of bytes: launch and three dependent reads - offsets, length, page).  Without
+// queries a token's own instructions bound it (65536 tokens, e4m3: 51 us); products with
+// a reciprocal and a check for ties in place of its 18 divisions a lane: 56 us.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <math.h>
@@ -238,8 +240,13 @@ cudaError_t launch_append(const mla_append_args_t* a, cudaStream_t stream) {
   p.H = a->H;
   p.max_pages = a->max_pages_per_seq;
   p.num_pages = a->num_pages;
-  // a warp per 32 heads, so that a lane has about 8 pieces
+  // A warp per 32 heads, so that a lane has about 8 pieces; twice as many while that leaves
+  // the GPU with at most two CTAs an SM (64 tokens, 128 heads: 2.8 us against 3.5; 16351
+  // tokens in an e4m3 cache 121 us against 98).
   p.warps_per_token = a->H > 64 ? 4 : a->H > 32 ? 2 : 1;
+  while (p.warps_per_token < kWarps && 8 * p.warps_per_token <= a->H &&
+         (int64_t)a->n_tok * 2 * p.warps_per_token <= (int64_t)kWarps * 2 * device_sm_count())
+    p.warps_per_token *= 2;
   p.turn = 0.15915494309189533577;
   for (int k = 0; k < 5; ++k) p.fall[k] = exp2(-(double)(1 << k) / (kDr / 2) * log2((double)a->rope_base));
   const int tokens = kWarps / p.warps_per_token;

@@ -328,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_dec<80>();  // 384 threads launched with 168 registers: 128 x 80 + 256 x 208 is within that
     if (warp == 3) {
       // =========================== plans ===========================
-      if (blockIdx.x == 0) packed_check(p.cu, p.B, p.n_tok, p.status, lane, 32);
       const uint32_t answer = sa + C::kBars + kNextOff;
       const int cu0 = min(max(p.cu[0], 0), p.n_tok), cu1 = min(max(p.cu[p.B], 0), p.n_tok);
       // the sequence of row r, for rows [cu0, cu1): its bounds
@@ -427,6 +426,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           pl->n = max(pl->to[0], pl->to[1]);
         }
         arrive(B_PLAN + (w & 1));
+        if (w == 0 && blockIdx.x == 0) packed_check(p.cu, p.B, p.n_tok, p.status, lane, 32);
         // The next block is claimed when the loads of this one begin, not before: a block
         // held in store is one that an idle SM cannot take.
         if (!wait(B_BEGUN, w)) break;

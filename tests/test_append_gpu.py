@@ -280,3 +280,42 @@ def test_append_far_pages(cuda_lib, kv):
     assert cuda_lib.mla_get_status(ws) == 0
     check(x, dict(cache=cache[shift:].cpu(), scale=None if scale is None else scale[shift:].cpu(), k=k_out.cpu(), q=q_out.cpu()))
     assert not bool(cache[:shift].view(torch.uint8).any())
+
+
+@pytest.mark.parametrize("kv", ["fp8", "q8_0", "q4_0"])
+def test_append_codes_at_ties(cuda_lib, kv):
+    """Values whose quotients are exactly between two codes, a hair beside that, and
+    subnormal; rows from tiny to huge; each bit of the latents' codes and scales."""
+    x = make([64], [64], 1, kv, seed=13)
+    g = torch.Generator().manual_seed(13)
+    rows = torch.zeros(64, 576)
+    for i in range(64):
+        e = 2.0 ** (2 * i - 64)
+        if kv == "fp8":
+            v = (torch.randint(-120, 121, (576,), generator=g).float() + 0.0) / 16      # ties of three mantissa bits
+            v[::7] = torch.randint(-15, 16, (83,), generator=g).float() * 2.0 ** -10    # of the smallest steps
+            v[5] = 448.0
+        else:
+            levels = 127 if kv == "q8_0" else 7
+            v = torch.randint(-levels, levels, (576,), generator=g).float() + 0.5
+            v[::3] *= 1 + 2.0 ** -7 * torch.randint(-1, 2, (192,), generator=g).float()
+            v[::32] = levels
+        rows[i] = v * e
+    if kv != "fp8":
+        rows[:, :] = rows.clamp(-3e4, 3e4)
+    x["joint"] = rows.to(bf16)
+    x["joint"][:, 512:] = 0
+    got = run(cuda_lib, x)
+    assert got["status"] == 0
+    check(x, got)
+    page = int(x["table"][0, 0])
+    c = om.bf16_to_f64(bf16_bits(x["joint"]))
+    n = 256 if kv == "q4_0" else 512          # (the key's zeros may come out of the rotation as -0)
+    for i in range(64):
+        if kv == "fp8":
+            code, sc = cw.quantise_row_e4m3(c[i])
+            assert got["scale"][page, i].item() == sc
+        else:
+            code, sc = (cw.quantise_row_q8_0 if kv == "q8_0" else cw.quantise_row_q4_0)(c[i])
+            assert np.array_equal(f16_bits(got["scale"])[page, i][:16], np.asarray(sc, np.float16).view(np.uint16)[:16])
+        assert np.array_equal(bits(got["cache"])[page, i][:n].view(np.uint8), np.asarray(code)[:n].view(np.uint8))
