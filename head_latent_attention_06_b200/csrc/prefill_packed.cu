@@ -258,6 +258,7 @@ MLA_DEVI int next_block(uint32_t answer) {
       : "memory");
   return x;
 }
+MLA_DEVI void prefetch_map(const void* map) { asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory"); }
 // 32 bytes to global memory
 MLA_DEVI void stg256(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
@@ -298,6 +299,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
   };
 
+  if (warp == 2 && lane == 0) {
+    prefetch_map(&tm_qn);
+    prefetch_map(&tm_kn);
+    prefetch_map(&tm_v);
+    if constexpr (PE) {
+      prefetch_map(&tm_qp);
+      prefetch_map(&tm_kp);
+    }
+  }
+  int cu0 = 0, cu1 = 0;  // of the planning warp
+  if (warp == 3) {
+    pdl_wait();
+    cu0 = min(max(p.cu[0], 0), p.n_tok);
+    cu1 = min(max(p.cu[p.B], 0), p.n_tok);
+  }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
     issued[0] = issued[1] = issued[2] = 0;
@@ -329,7 +345,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 3) {
       // =========================== plans ===========================
       const uint32_t answer = sa + C::kBars + kNextOff;
-      const int cu0 = min(max(p.cu[0], 0), p.n_tok), cu1 = min(max(p.cu[p.B], 0), p.n_tok);
       // the sequence of row r, for rows [cu0, cu1): its bounds
       auto find = [&](int r, int& lo, int& hi) {
         int a = 0, z = p.B;  // the count of entries cu[1 .. B] that are <= r
