@@ -24,10 +24,11 @@
 // tile 1280 cycles of products (d_r = 64; 1024 without) stand against some 1500 of
 // softmax, 1024 of them exponentials at the special-function units' rate.
 //
-// Measured (us; CUDA events, back to back, 40 passes): one prompt of 4096 tokens, 128
-// heads 557 (1.23 PFLOP/s, 0.76 of the measured cuBLAS burst rate); 7 prompts of
-// 5120 tokens, 128 heads 357; 5 prompts of 7001 tokens, 32 heads in groups of 4 without
-// the RoPE part 137; 67 prompts of 8191 tokens, 16 heads 63; one of 17 tokens 8.
+// Measured (us; in long runs back to back, and over a few tens of passes): one prompt of
+// 4096 tokens, 128 heads 630 and 555 (1.09 and 1.24 PFLOP/s; cuBLAS 1.38 and 1.62); 7
+// prompts of 5120 tokens, 128 heads 391 and 354; 5 prompts of 7001 tokens, 32 heads in
+// groups of 4 without the RoPE part 141 and 125; 67 prompts of 8191 tokens, 16 heads 57
+// and 55; one of 17 tokens 6.8.
 #include <math_constants.h>
 
 #include "packed.cuh"

@@ -3,6 +3,9 @@ verification (CPU): the C ABI's host checks on made-up pointers, none of which
 reaches a launch, and the tensor builders' checks."""
 
 import ctypes
+import os
+import shutil
+import subprocess
 
 import numpy as np
 import pytest
@@ -135,6 +138,53 @@ def test_workspace_sizes(lib):
     assert mla.mla_verify_workspace_size(verify_args()) == 256
     with pytest.raises(mla.MlaError, match="MLA_ERR_UNSUPPORTED"):
         mla.mla_append_workspace_size(append_args(d_r=63))
+
+
+C_PROGRAM = r"""
+#include <stdio.h>
+#include <string.h>
+#include "mla.h"
+
+int main(void) {
+  /* host-side checks only: nothing here reaches a CUDA launch */
+  size_t bytes = 0;
+  mla_append_args_t a;
+  memset(&a, 0, sizeof a);
+  a.n_tok = 8; a.B = 2; a.H = 16; a.d_c = MLA_D_C; a.d_r = MLA_D_R; a.page_size = MLA_PAGE_SIZE;
+  a.num_pages = 4; a.max_pages_per_seq = 2; a.kv_dtype = MLA_KV_Q4_0; a.rope_base = 10000.f;
+  if (mla_append_workspace_size(&a, &bytes) != MLA_OK || bytes != 256) return 1;
+  if (mla_append_kv(&a, 0) != MLA_ERR_INVALID_VALUE) return 2;          /* no workspace */
+  mla_prefill_packed_args_t p;
+  memset(&p, 0, sizeof p);
+  p.n_tok = 8; p.B = 2; p.H = 16; p.H_kv = 4; p.d_n = MLA_D_QK_NOPE; p.d_v = MLA_D_V; p.causal = 1;
+  p.softmax_scale = 0.0884f;
+  if (mla_prefill_packed_workspace_size(&p, &bytes) != MLA_OK || bytes != 256) return 3;
+  p.d_r = 32;
+  if (mla_prefill_packed(&p, 0) != MLA_ERR_UNSUPPORTED) return 4;
+  mla_verify_args_t v;
+  memset(&v, 0, sizeof v);
+  v.B = 2; v.s_q = 4; v.V = 1000; v.dtype = MLA_PROB_BF16;
+  if (mla_verify_workspace_size(&v, &bytes) != MLA_OK || bytes != 256) return 5;
+  if (mla_verify_draft(&v, 0) != MLA_ERR_INVALID_VALUE) return 6;
+  if (strcmp(mla_status_string(MLA_ERR_BAD_TOKEN), "MLA_ERR_BAD_TOKEN") != 0) return 7;
+  printf("%d %d %d\n", (int)sizeof a, (int)sizeof p, (int)sizeof v);
+  return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="no C compiler")
+def test_c_program_calls_the_entry_points(tmp_path, lib):
+    """From plain C; the binding's structs are as large as the header's."""
+    src, exe = tmp_path / "p.c", tmp_path / "p"
+    src.write_text(C_PROGRAM)
+    d = os.path.dirname(mla.LIB_PATH)
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Werror", "-pedantic", "-I", os.path.join(os.path.dirname(d), "include"),
+                        str(src), "-o", str(exe), mla.LIB_PATH, f"-Wl,-rpath,{d}"], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.returncode
+    assert [int(n) for n in r.stdout.split()] == [ctypes.sizeof(t) for t in (mla.AppendArgs, mla.PrefillPackedArgs, mla.VerifyArgs)]
 
 
 # ------------------------------------------------------------------ builders
