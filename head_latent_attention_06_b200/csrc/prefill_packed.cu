@@ -844,8 +844,13 @@ cudaError_t launch_prefill_packed(const mla_prefill_packed_args_t* a, cudaStream
   p.blocks = (int)(((int64_t)a->n_tok + kRows - 1) / kRows);
   p.wait_ns = device_wait_limit_ns();
   p.wide = (reinterpret_cast<uintptr_t>(a->out) & 31u) == 0;  // the ABI asks for 16 bytes
+  // 16 key heads at a time: their keys and values stay in L2 while several blocks read
+  // them (8 / 16 / 32 heads, long runs: 404 / 393 / 400 us for the 7 prompts, 645 / 642 / 650
+  // for the long one).
   const int heads = kHeadGroup * p.share;
   p.group = heads < a->H ? heads : a->H;
+  // Sorting pays once an SM takes more than one block (it evens out the end: the 5 grouped
+  // prompts 168 -> 137 us); with fewer it would only delay the first.
   p.sorted = p.blocks <= kMaxSorted && (int64_t)p.blocks * a->H > device_sm_count();
   return a->d_r ? launch_tiles<true>(a, p, stream) : launch_tiles<false>(a, p, stream);
 }

@@ -319,3 +319,18 @@ def test_append_codes_at_ties(cuda_lib, kv):
             code, sc = (cw.quantise_row_q8_0 if kv == "q8_0" else cw.quantise_row_q4_0)(c[i])
             assert np.array_equal(f16_bits(got["scale"])[page, i][:16], np.asarray(sc, np.float16).view(np.uint16)[:16])
         assert np.array_equal(bits(got["cache"])[page, i][:n].view(np.uint8), np.asarray(code)[:n].view(np.uint8))
+
+
+def test_append_single_rows(cuda_lib):
+    """One token and one head: strides along them say nothing."""
+    x = make([1], [130], 1, "q8_0", seed=14)
+    d = {k: v.cuda() for k, v in x.items() if torch.is_tensor(v)}
+    one = lambda t, *shape: t.as_strided(shape, (0,) * (len(shape) - 1) + (1,), t.storage_offset())
+    k_out, q_out = torch.zeros(1, 64, dtype=bf16, device="cuda"), torch.zeros(1, 1, 64, dtype=bf16, device="cuda")
+    a = cuda_lib.make_append_args(c=one(d["joint"], 1, 512), k_pe=one(d["joint"][:, 512:], 1, 64), q_pe=one(d["q"], 1, 1, 64),
+                                  k_pe_out=one(k_out, 1, 64), q_pe_out=one(q_out, 1, 1, 64), kv_cache=d["cache"],
+                                  kv_scale=d["scale"], block_table=d["table"], cu_seqlens=d["cu"], seq_lens=d["lens"])
+    ws = cuda_lib.alloc_workspace(a)
+    cuda_lib.mla_append_kv(a)
+    assert cuda_lib.mla_get_status(ws) == 0
+    check(x, dict(cache=d["cache"].cpu(), scale=d["scale"].cpu(), k=k_out.cpu(), q=q_out.cpu()))

@@ -359,3 +359,23 @@ def test_packed_prefill_agrees_with_the_cached_form(cuda_lib):
     d = 192 * 2.0 ** -23 * want[3] + 2.0 ** -7 * want[3]
     tol = 2 * ((2.0 ** -8 + 2.1 * d + 2.0 ** -15)[..., None] * want[2] + 2.0 ** -8 * np.abs(want[0])) + 2.0 ** -7 * want[2]
     assert (np.abs(to_np(step.out) - to_np(ref.out).reshape(n, H, 128)) <= tol).all()
+
+
+def test_packed_output_at_16_bytes_and_single_rows(cuda_lib):
+    """An output that starts 16 bytes into a sector; inputs of one row and one head whose
+    strides along those say nothing."""
+    x = make([300, 20], 5, 5, 64, seed=18)
+    want = oracle_of(x, True)
+    room = torch.full((320 * 5 * 128 + 16,), 7.0, dtype=bf16, device="cuda")
+    x["out"] = room[8:8 + 320 * 5 * 128].view(320, 5, 128)
+    assert x["out"].data_ptr() % 32 == 16
+    assert run(cuda_lib, x) == 0
+    check(x, want)
+    assert bool((room[:8] == 7).all()) and bool((room[-8:] == 7).all())
+    x = make([1], 1, 1, 64, seed=19)
+    want = oracle_of(x, True)
+    for name in ("q_nope", "q_pe", "k_nope", "v"):
+        x[name] = x[name].as_strided(x[name].shape, (0, 0, 1), x[name].storage_offset())
+    x["k_pe"] = x["k_pe"].as_strided((1, 64), (0, 1), x["k_pe"].storage_offset())
+    assert run(cuda_lib, x) == 0
+    check(x, want)
