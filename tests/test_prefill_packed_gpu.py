@@ -131,6 +131,22 @@ def test_packed_more_blocks_than_the_gpu_holds(cuda_lib, causal):
     untouched(x)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,H,H_kv,d_r,kw", [
+    ([127, 128, 129], 80, 80, 64, {}),
+    ([255, 256, 257], 52, 4, 0, dict(tail=1)),
+    ([3, 130, 300, 64, 1, 200], 52, 13, 64, dict(fused=False)),
+    ([40] * 14, 60, 60, 0, dict(head=2, tail=9)),
+    ([200, 177], 76, 38, 64, dict(gain=6.0)),
+])
+def test_packed_grids_that_fill_the_gpu(cuda_lib, lens, H, H_kv, d_r, kw, causal):
+    """More (block, head) pairs than multiprocessors, of few rows each."""
+    x = make(lens, H, H_kv, d_r, **kw)
+    assert run(cuda_lib, x, causal) == 0
+    check(x, oracle_of(x, causal))
+    untouched(x)
+
+
 def test_packed_more_rows_than_are_sorted(cuda_lib):
     """More than 128 blocks of rows: taken from the end on."""
     x = make([20000, 13800, 1, 700], 4, 1, 0, seed=12)
@@ -155,8 +171,8 @@ def test_packed_offsets_beyond_32_bits(cuda_lib):
 def test_packed_scores_that_keep_rising(cuda_lib):
     """Scores that rise along the prompt by less than, about and far more than the range
     that the running reference leaves open, and one that falls."""
-    for steps in (0.02, 0.2, 2.0, -0.2):
-        x = make([700], 2, 1, 0, seed=14)
+    for steps, H in ((0.02, 2), (0.2, 2), (2.0, 2), (-0.2, 2), (0.2, 54), (2.0, 54)):
+        x = make([700], H, 1, 0, seed=14)
         x["q_nope"].zero_()
         x["k_nope"].zero_()
         x["q_nope"][:, :, 0] = 128 ** 0.5                       # the score is k's first value
@@ -239,12 +255,13 @@ def check_rows(x, rows):
         check(part, (o, lse, mass, size))
 
 
+@pytest.mark.parametrize("H", [2, 80])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_packed_unseen_values_have_no_effect(cuda_lib, bad):
+def test_packed_unseen_values_have_no_effect(cuda_lib, bad, H):
     """NaN and infinities in tokens that a row does not see: later tokens of its
     prompt, other prompts, rows of no prompt.  Rows that see them are not compared."""
     lens = [130, 90, 200]
-    x = make(lens, 2, 2, 64, seed=4, head=1, tail=30)
+    x = make(lens, H, H, 64, seed=4, head=1, tail=30)
     ref = oracle_of(x, True)
     spoilt = [0, 100, 131, 220, 400, 421, 425, 450]
     for t in spoilt:
