@@ -122,6 +122,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     first_bad[1] = bad_n;
   }
   __syncthreads();
+  if (cluster > 1) sm100::cluster_arrive();
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const int x = p.draft[(int64_t)b * most + i];
     if (x < 0 || x >= p.V) {
@@ -132,10 +133,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     if (!((double)p.u_accept[(int64_t)b * most + i] * qx < (double)ld(P, i * p.p_row + x))) atomicMin(&first_bad[0], i);
   }
   __syncthreads();
+  if (cluster > 1) sm100::cluster_wait();  // the first CTA runs: its shared memory may be written
   const int a = first_bad[0], bad = first_bad[1];
   int next = -1;
   if (!bad) {
-    // every CTA of the cluster is here: they read the same arguments
     const T* pr = P + a * p.p_row;
     const T* qr = a < n && Q ? Q + a * p.q_row : nullptr;
     const int certain = a < n && !Q ? p.draft[(int64_t)b * most + a] : -1;  // draft of probability one
@@ -253,8 +254,13 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
       const int j = seg * kSeg + 32 * pick(parts[lane], goal, run, lane);
       next = j + pick(value(j + lane), goal, run, lane);
     }
-  } else if (rank != 0 || warp != 0) {
-    return;
+  } else {
+    // the first CTA stays until the others, whatever they read, have written their last sum
+    if (cluster > 1) {
+      sm100::cluster_arrive();
+      sm100::cluster_wait();
+    }
+    if (rank != 0 || warp != 0) return;
   }
   // outputs, by one warp
   const int kept = bad ? 0 : a;

@@ -191,6 +191,23 @@ def test_verify_reports_bad_arguments(cuda_lib, field, value, code):
         assert run(cuda_lib, x)[0] == 0
 
 
+@pytest.mark.parametrize("V", [9000, 100003])
+def test_verify_bad_sequences_among_clusters(cuda_lib, V):
+    """Sequences that end early beside others whose blocks share their sums, many times over."""
+    x = make(24, 2, V, seed=13, ragged=True)
+    x["num_draft"][3::4] = 2
+    want = oracle_of(x)
+    x["num_draft"][1::4] = torch.tensor([3, -1, 3, -7, 9, 3], dtype=i32)
+    x["draft_tokens"][3::4, 0] = torch.tensor([V, -1, V + 9, -5, 2 ** 30, V], dtype=i32)
+    for _ in range(20):
+        status, tokens, acc, new = run(cuda_lib, x)
+        assert status in (8, 9)
+        assert (tokens[1::2] == -1).all() and (acc[1::2] == 0).all()
+        np.testing.assert_array_equal(new[1::2], x["seq_lens"][1::2].numpy())
+        for got, ref in ((tokens, want[0]), (acc, want[1]), (new, want[2])):
+            np.testing.assert_array_equal(got[::2], ref[::2])
+
+
 def test_verify_on_another_stream_and_in_a_graph(cuda_lib):
     x = make(5, 3, 9000, seed=7, ragged=True)
     want = oracle_of(x)
