@@ -60,6 +60,10 @@ struct Is {
   static constexpr bool value = kOn;
 };
 
+// What a drafting probability takes from x >= 0, which is no NaN: at most all of it; a NaN
+// takes all, a negative value nothing
+MLA_DEVI float less_of(float q, float x) { return fmaxf(fminf(q, x), 0.f); }
+
 // What a value adds: only what is positive (a NaN is not)
 MLA_DEVI double weight(double w) { return w > 0.0 ? w : 0.0; }
 
@@ -159,8 +163,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
 #pragma unroll
         for (int k = 0; k < kN; ++k) {
           // p - min(q, p) is zero or positive, and what rounding took from it comes out
-          // exactly since p >= q (Dekker); then the running sum with its rounding error
-          const float x = decltype(whole)::value || j + 32 * k < p.V ? fmaxf(pv[k], 0.f) : 0.f, y = fminf(qv[k], x);
+          // exactly since p >= q >= 0 (Dekker); then the running sum with its rounding error
+          const float x = decltype(whole)::value || j + 32 * k < p.V ? fmaxf(pv[k], 0.f) : 0.f, y = less_of(qv[k], x);
           const float d = __fsub_rn(x, y), e = __fsub_rn(__fsub_rn(x, d), y);
           float f;
           acc = two_sum(acc, d, f);
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
         const int l = pick_of(own, upto, goal, run);
         seg = __shfl_sync(0xffffffffu, s0, l);
         const int many = __shfl_sync(0xffffffffu, s1, l) - seg;
-        if (per > 1) seg += pick(lane < many ? sums[row][seg + lane] : 0.0, goal, run, lane);
+        if (per > 1) seg += max(pick(lane < many ? sums[row][seg + lane] : 0.0, goal, run, lane), 0);
       }
       if (lane == 0) {
         found[0] = seg;
@@ -235,8 +239,9 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     const int seg = found[0], row = found[1];
     // the segment's values again, 128 to a warp, in 32 parts of 32
     auto value = [&](int j) {
-      const float pv = ld(pr, min(j, p.V - 1)), qv = qr ? ld(qr, min(j, p.V - 1)) : j == certain ? 1.f : 0.f;
-      return j < p.V ? weight((double)pv - (row ? 0.0 : (double)qv)) : 0.0;
+      const float x = fmaxf(ld(pr, min(j, p.V - 1)), 0.f);
+      const float qv = row ? 0.f : qr ? ld(qr, min(j, p.V - 1)) : j == certain ? 1.f : 0.f;
+      return j < p.V ? (double)x - (double)less_of(qv, x) : 0.0;
     };
     if (seg >= 0) {
       double x[kSeg / 32 / kWarps];
@@ -251,8 +256,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     __syncthreads();
     if (warp != 0) return;
     if (seg >= 0) {
-      const int j = seg * kSeg + 32 * pick(parts[lane], goal, run, lane);
-      next = j + pick(value(j + lane), goal, run, lane);
+      const int part = pick(parts[lane], goal, run, lane);
+      const int j = seg * kSeg + 32 * max(part, 0);
+      const int at = pick(value(j + lane), goal, run, lane);
+      if (part >= 0 && at >= 0) next = j + at;  // a sum above zero has a value above zero: else the rows changed meanwhile
     }
   } else {
     // the first CTA stays until the others, whatever they read, have written their last sum

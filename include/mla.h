@@ -575,10 +575,11 @@ mla_status_t mla_verify_workspace_size(const mla_verify_args_t* args, size_t* by
  *   w_j = max(p_a(j) - q_a(j), 0) when a < n (p_a(j) where no w_j is positive), else p_n(j)
  *   next token = the smallest j with w_0 + .. + w_j > u_sample (w_0 + .. + w_(V-1))
  * num_accepted = a, tokens = x_0 .. x_(a-1), next, -1 .., new_lens = seq_lens - (n - a).
- * Differences, sums and comparisons are in fp64, so the result does not depend on
- * the order of summation but for u within some 1e-15 of a boundary.  A weight
- * that is not positive (or NaN) counts as zero; the next token is -1 when nothing
- * is left or the sum is not finite.  A draft outside [0, V) (MLA_ERR_BAD_TOKEN)
+ * Differences are exact, the sums carry the rounding errors of 32-bit steps along
+ * and are joined in fp64: u within some 1e-12 of a boundary, relative to the sum,
+ * may fall on either side, the same side every time.  Probabilities below zero
+ * count as zero in w, and so does a weight that is NaN; the next token is -1 when
+ * nothing is left, a p_a(j) is infinite or the sum is beyond fp32.  A draft outside [0, V) (MLA_ERR_BAD_TOKEN)
  * or num_draft outside [0, s_q - 1] (MLA_ERR_BAD_SEQ_LEN) is recorded in the
  * workspace's status word and that sequence gets num_accepted = 0, tokens = -1
  * and new_lens = seq_lens.

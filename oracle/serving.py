@@ -72,18 +72,19 @@ def verify_draft(p, q, draft, num, u_accept, u_sample, seq_lens):
                 break
             tokens[b, a] = x
             a += 1
-        target = p[b, a].astype(np.float64)
+        target = np.maximum(p[b, a].astype(np.float64), 0.0)
         w = target.copy()
         if a < n:
             if q is None:
                 w[int(draft[b, a])] -= 1.0
             else:
-                w = w - q[b, a].astype(np.float64)
+                with np.errstate(invalid="ignore"):
+                    w = w - np.maximum(q[b, a].astype(np.float64), 0.0)
         w = np.where(w > 0, w, 0.0)
         if a < n and not w.sum() > 0:
             w = np.where(target > 0, target, 0.0)
         sums = np.cumsum(w)
-        if sums[-1] > 0 and np.isfinite(sums[-1]):
+        if sums[-1] > 0 and np.isfinite(sums[-1]) and not np.isposinf(target).any():
             tokens[b, a] = int(np.searchsorted(sums, float(u_sample[b]) * sums[-1], side="right"))
         accepted[b], new_lens[b] = a, new_lens[b] - (n - a)
     return tokens, accepted, new_lens

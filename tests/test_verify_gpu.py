@@ -1,7 +1,9 @@
 """GPU parity of the draft verification (mla_verify_draft) against the fp64 oracle:
 all results are whole numbers and have to be equal.  The oracle sums in another
-order than the kernel; both are within some 10^-15 of the exact sum, so a random
-u_sample falls between them with a chance near 10^-10 over all cases here."""
+order than the kernel, which is within 2^-38 of the exact sum: 32 differences carry their
+errors, each below 2^-24 of the sum, and joining the 32 errors costs at most 32 roundings of
+2^-24 of 33 such errors.  A random u_sample falls between the two sums of some
+token with a chance below V 2^-38: below 10^-3 over the some 10^7 values here."""
 
 import numpy as np
 import pytest
@@ -169,6 +171,33 @@ def test_verify_not_a_number(cuda_lib):
     for b in (0, 3):
         np.testing.assert_array_equal(tokens[b], want[0][b])
         assert acc[b] == want[1][b] and new[b] == want[2][b]
+
+
+@pytest.mark.parametrize("dtype", [f32, bf16])
+@pytest.mark.parametrize("V", [1, 50, 1024, 1100, 40000])
+def test_verify_outside_the_range_of_probabilities(cuda_lib, V, dtype):
+    """Values below zero count as zero on both sides, infinities and NaN among them:
+    rows that are all negative, a few of them, a draft row of infinities, of NaN."""
+    x = make(8, 1, V, dtype, seed=14)
+    x["u_accept"][:] = 1 - 2.0 ** -24
+    x["target_probs"][0] = -0.1
+    x["draft_probs"][0] = -0.2
+    x["target_probs"][1] *= -1
+    x["draft_probs"][1] *= -2
+    x["target_probs"][2, :, ::2] *= -1
+    x["draft_probs"][2, :, ::3] *= -1
+    x["draft_probs"][3] *= -1
+    x["draft_probs"][4] = float("inf")
+    x["draft_probs"][5] = float("nan")
+    x["draft_probs"][6, :, ::5] = -float("inf")
+    x["target_probs"][6, :, ::7] = -float("inf")
+    x["target_probs"][7, :, V // 2] = float("inf")
+    x["draft_probs"][7] = float("inf")
+    at = x["draft_tokens"][:4, 0].long()
+    x["draft_probs"][torch.arange(4), 0, at] = 2.0                                 # rejected
+    want = oracle_of(x)
+    check(run(cuda_lib, x), want)
+    assert (want[1][[0, 1, 2, 3, 4, 5, 7]] == 0).all() and (want[0][[0, 1, 7], 0] == -1).all()
 
 
 @pytest.mark.parametrize("field,value,code", [("draft_tokens", 2000, 9), ("draft_tokens", -1, 9), ("num_draft", 3, 8),
