@@ -19,8 +19,8 @@
 //
 // Measured: 256 sequences, 3 drafts, 128000 fp32 values 46 us = 4.8 TB/s (0.73 of the
 // copy rate; sequences whose drafts were all accepted read one row, the others two, and
-// the search at the end is not hidden); 33 sequences, 100003 bf16 values 9 us; one
-// sequence, 32000 values 6.1 us in a CUDA graph, of which 2 us are the dependent reads of
+// the search at the end is not hidden); 33 sequences, 100003 bf16 values 8.7 us in a CUDA graph; one
+// sequence, 32000 values 5.8 us in a CUDA graph, of which 2 us are the dependent reads of
 // draft, probabilities and row and 2.5 us the search.
 #include <math.h>
 
@@ -111,6 +111,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
   __shared__ int first_bad[2];          // first rejected draft; whether an argument is bad
   __shared__ int found[2];              // the segment of the next token (-1: none), the row of sums it came from
   // No early trigger: new_lens may be the lengths that a decode reads before it waits.
+  // Before anything else, each block says that it runs (nothing to release by that).
+  if (cluster > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t rank = cluster > 1 ? sm100::cluster_ctarank() : 0;
@@ -126,7 +128,6 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     first_bad[1] = bad_n;
   }
   __syncthreads();
-  if (cluster > 1) sm100::cluster_arrive();
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const int x = p.draft[(int64_t)b * most + i];
     if (x < 0 || x >= p.V) {
@@ -240,8 +241,8 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const VerifyParams 
     // the segment's values again, 128 to a warp, in 32 parts of 32
     auto value = [&](int j) {
       const float x = fmaxf(ld(pr, min(j, p.V - 1)), 0.f);
-      const float qv = row ? 0.f : qr ? ld(qr, min(j, p.V - 1)) : j == certain ? 1.f : 0.f;
-      return j < p.V ? (double)x - (double)less_of(qv, x) : 0.0;
+      const float qv = qr ? ld(qr, min(j, p.V - 1)) : j == certain ? 1.f : 0.f;  // loaded whatever `row` says
+      return j < p.V ? (double)x - (row ? 0.0 : (double)less_of(qv, x)) : 0.0;
     };
     if (seg >= 0) {
       double x[kSeg / 32 / kWarps];
