@@ -485,6 +485,10 @@ mla_status_t mla_append_kv(const mla_append_args_t* a, void* stream) {
                                 {a->q_pe_out_head, a->H}};
   for (const auto& s : strides)
     if ((st = check_stride(s[0], s[1])) != MLA_OK) return st;
+  // outputs whose rows or heads overlap would be written twice
+  if ((a->k_pe_out && a->n_tok > 1 && a->k_pe_out_tok < kDr) || (a->H > 0 && a->n_tok > 1 && a->q_pe_out_tok < kDr) ||
+      (a->H > 1 && a->q_pe_out_head < kDr))
+    return MLA_ERR_INVALID_VALUE;
   // in place means the same elements: another stride would read what was written
   if (a->k_pe_out == a->k_pe && a->n_tok > 1 && a->k_pe_out_tok != a->k_pe_tok) return MLA_ERR_INVALID_VALUE;
   if (a->H > 0 && a->q_pe_out == a->q_pe &&

@@ -476,7 +476,8 @@ mla_status_t mla_append_workspace_size(const mla_append_args_t* args, size_t* by
  * A length below n_b or beyond the block table, or cu_seqlens out of order
  * (MLA_ERR_BAD_SEQ_LEN), or a page id outside the cache (MLA_ERR_BAD_BLOCK_TABLE)
  * is recorded in the workspace's status word and the token is skipped, its
- * outputs included.  Gives no early start to the kernels enqueued after it.
+ * outputs included.  But for the two that may be written over themselves, outputs
+ * overlap neither an input nor themselves.  Gives no early start to the kernels enqueued after it.
  */
 mla_status_t mla_append_kv(const mla_append_args_t* args, void* stream);
 
@@ -582,7 +583,7 @@ mla_status_t mla_verify_workspace_size(const mla_verify_args_t* args, size_t* by
  * nothing is left, a p_a(j) is infinite or the sum is beyond fp32.  A draft outside [0, V) (MLA_ERR_BAD_TOKEN)
  * or num_draft outside [0, s_q - 1] (MLA_ERR_BAD_SEQ_LEN) is recorded in the
  * workspace's status word and that sequence gets num_accepted = 0, tokens = -1
- * and new_lens = seq_lens.
+ * and new_lens = seq_lens.  Outputs overlap no input (new_lens may be seq_lens).
  */
 mla_status_t mla_verify_draft(const mla_verify_args_t* args, void* stream);
 

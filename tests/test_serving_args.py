@@ -83,6 +83,9 @@ REFUSED = [
         (dict(c_tok=577), MISALIGNED), (dict(c_tok=0), INVALID), (dict(q_pe_head=-192), INVALID),
         (dict(q_pe_tok=1 << 38), UNSUPPORTED), (dict(k_pe_out_tok=64), INVALID), (dict(q_pe_out_head=64), INVALID),
         (dict(q_pe_out_tok=64 * 16), INVALID),
+        # rows or heads of an output over one another (written over themselves, so that no other rule refuses them)
+        (dict(k_pe_out_tok=56, k_pe_tok=56), INVALID), (dict(q_pe_out_tok=8, q_pe_tok=8), INVALID),
+        (dict(q_pe_out_head=32, q_pe_head=32), INVALID),
     ]),
     (packed_args, "mla_prefill_packed", [
         (dict(B=-1), INVALID), (dict(H=0), INVALID), (dict(H_kv=0), INVALID), (dict(n_tok=-1), INVALID),
