@@ -206,11 +206,14 @@ class SpeculativeStep(DecodeStep):
     appends their latents and rotated RoPE keys (latent [B * s_q][576], q_pe
     [B][s_q][H][64], not yet rotated), attends causally, and, once the model has
     turned the output into probabilities, verifies the drafts; ``seq_lens`` (the
-    drafts included) then loses the rejected ones in place."""
+    drafts included) then loses the rejected ones in place.  q_pe is read where it
+    stands on every run, so its first two dimensions have to merge without a copy."""
 
     def __init__(self, *, latent, q_nope, q_pe, w_uk, w_uv, kv_cache, kv_scale, block_table, seq_lens,
                  softmax_scale, rope_base=10000.0, num_splits=0, max_seq_len=0, out=None):
         B, s_q, H, _ = q_pe.shape
+        if B > 1 and s_q > 1 and q_pe.stride(0) != s_q * q_pe.stride(1):
+            raise ValueError("q_pe's sequences must follow one another at its token stride")
         dev = q_pe.device
         rotated = torch.empty_like(q_pe, memory_format=torch.contiguous_format)
         super().__init__(q_nope=q_nope, q_pe=rotated, w_uk=w_uk, w_uv=w_uv, kv_cache=kv_cache, kv_scale=kv_scale,
@@ -235,9 +238,9 @@ class SpeculativeStep(DecodeStep):
         self.append(stream)
         return super().run(stream)
 
-    def verify(self, *, target_probs, draft_probs, draft_tokens, u_accept, u_sample, num_draft=None, stream=None):
+    def verify(self, *, target_probs, draft_probs, draft_tokens, u_accept, u_sample, stream=None):
         args = make_verify_args(target_probs=target_probs, draft_probs=draft_probs, draft_tokens=draft_tokens,
-                                u_accept=u_accept, u_sample=u_sample, num_draft=num_draft, seq_lens=self.seq_lens,
+                                u_accept=u_accept, u_sample=u_sample, seq_lens=self.seq_lens,
                                 tokens=self.tokens, num_accepted=self.num_accepted, new_lens=self.seq_lens,
                                 workspace=self.verify_workspace)
         mla_verify_draft(args, stream)

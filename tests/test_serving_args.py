@@ -318,3 +318,20 @@ def test_oracle_verification_draws_from_the_target():
 def test_oracle_append_positions():
     rows, seq, pos = serving.packed_positions([2, 4, 4, 7], [10, 5, 3])
     assert rows.tolist() == [2, 3, 4, 5, 6] and seq.tolist() == [0, 0, 2, 2, 2] and pos.tolist() == [8, 9, 0, 1, 2]
+
+
+def test_speculative_step_takes_no_copy_of_its_queries():
+    """Queries whose sequences do not follow one another would be copied once and then be stale."""
+    from head_latent_attention_06_b200.step import SpeculativeStep
+    q = torch.zeros(3, 2, 4, 192, dtype=torch.bfloat16)
+    names = ("latent", "q_nope", "w_uk", "w_uv", "kv_cache", "kv_scale", "block_table", "seq_lens")
+    for bad in (q.transpose(0, 1)[..., 128:], q[:, :1].expand(3, 2, 4, 192)[..., 128:]):
+        with pytest.raises(ValueError, match="q_pe"):
+            SpeculativeStep(q_pe=bad, softmax_scale=1.0, **dict.fromkeys(names))
+
+
+def test_speculative_step_verifies_all_its_drafts():
+    """The step appends s_q tokens of every sequence, so all of them have s_q - 1 drafts."""
+    import inspect
+    from head_latent_attention_06_b200.step import SpeculativeStep
+    assert "num_draft" not in inspect.signature(SpeculativeStep.verify).parameters
