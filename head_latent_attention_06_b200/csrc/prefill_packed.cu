@@ -765,8 +765,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (mine && p.lse) p.lse[orow] = inv == 0.f ? -CUDART_INF_F : (m_used + log2f(l)) * 0.6931471805599453f;
       // An infinite or NaN value that a row does not see has met its zero weight in the
       // product with V (0 x inf): such rows, and those that see one, are done over from
-      // the definition.
-      const bool odd = mine && (bad != 0.f || !(fabsf(l) < CUDART_INF_F));
+      // the definition.  So are those whose weights add up to far less than the one that
+      // the reference stands for: beyond scores of some 2^28 the reference's own rounding
+      // moves the exponents by that much, down to weights that are all flushed to zero.
+      const bool lost = l < 1.f / kRescale && m_used != -CUDART_INF_F;
+      const bool odd = mine && (bad != 0.f || !(fabsf(l) < CUDART_INF_F) || lost);
       __syncwarp();
       for (uint32_t again = __ballot_sync(0xffffffffu, odd); again; again &= again - 1) {
         const int r = __ffs(again) - 1;

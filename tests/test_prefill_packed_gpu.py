@@ -396,3 +396,51 @@ def test_packed_output_at_16_bytes_and_single_rows(cuda_lib):
     x["k_pe"] = x["k_pe"].as_strided((1, 64), (0, 1), x["k_pe"].storage_offset())
     assert run(cuda_lib, x) == 0
     check(x, want)
+
+
+def top_residues(x, causal):
+    """Per row and head of a batch whose values are the same along a query and along a key
+    (shared by all heads, d_r = 0): how far the top score, times the scale in base 2, lies
+    above its own rounding to fp32."""
+    a, b = x["q_nope"][..., 0].double().cpu().numpy(), x["k_nope"][:, 0, 0].double().cpu().numpy()
+    scale2 = np.float32(np.float32(1 / 128 ** 0.5) * np.float32(1.4426950408889634))
+    res = np.zeros(a.shape)
+    cu = x["cu_seqlens"].tolist()
+    for lo, hi in zip(cu, cu[1:]):
+        for t in range(lo, hi):
+            keys = b[lo:t + 1 if causal else hi]
+            s = 128 * np.where(a[t] > 0, a[t] * keys.max(), a[t] * keys.min())
+            exact = s * float(scale2)                  # 24 and 23 bits: exact in 64
+            res[t] = exact - exact.astype(np.float32)
+    return res
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("small", [1.0, 2.0 ** -90])
+def test_packed_scores_beyond_the_exponent_range(cuda_lib, small, causal):
+    """Finite scores so large (some 2^26 to 2^37) that their rounding to fp32 takes away or
+    adds more than the range of an exponential: the top key alone has weight, or the keys
+    that share the top score, for every row, of one key tile or several.
+
+    A score is 128 equal products of 8-bit by 8-bit significands: exact in fp32 whatever the
+    order.  Two that differ do so by at least 200 2^7 128 / sqrt(128) > 10^5, so all other
+    weights are zero in 64 bits too and the top ones equal; their sum with v and its
+    quotient by their number take some eight fp32 roundings (2^-20) of the mean |v|, the output half
+    a bf16 step (2^-8).  Where the reference's rounding is small the top weight is 2^r for the
+    residue r, no power of two, and is rounded to bf16 for the product with v while the sum that
+    divides it is not: another 2^-8 of the mean |v|.  lse: the scale's, the logarithm base's and the score's roundings,
+    seven of 2^-24, below 2^-21 of it."""
+    g = torch.Generator().manual_seed(20)
+    lens, H = [700, 90, 1], 3
+    x = make(lens, H, 1, 0, seed=20)
+    n = sum(lens)
+    sign = torch.where(torch.rand(n, H, generator=g) < 0.3, -1.0, 1.0)
+    x["q_nope"] = (200 * 500 ** torch.rand(n, H, generator=g) * sign).to(bf16).cuda()[..., None].repeat(1, 1, 128)
+    x["k_nope"] = (2e4 + 8e4 * torch.rand(n, 1, generator=g)).to(bf16).cuda()[..., None].repeat(1, 1, 128)
+    x["v"] = x["v"] * small
+    res = top_residues(x, causal)
+    assert (res < -126).sum() > 20 and (res > 60).sum() > 20 and ((res > -126) & (res < -8)).sum() > 20 and (np.abs(res) < 8).sum() > 20
+    assert run(cuda_lib, x, causal) == 0
+    o, lse, mass, _ = oracle_of(x, causal)
+    assert (np.abs(to_np(x["out"]) - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -20) * mass).all()
+    assert (np.abs(to_np(x["lse"]) - lse) <= 2.0 ** -21 * np.abs(lse)).all()
