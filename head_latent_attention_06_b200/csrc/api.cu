@@ -200,6 +200,22 @@ mla_status_t check_status_workspace(void* ws, size_t bytes) {
   return bytes < kStatusBytes ? MLA_ERR_WORKSPACE_TOO_SMALL : MLA_OK;
 }
 
+// Whether two of the vectors of `width` values at t * tok + h * head, t < n and h < H,
+// share a value; strides are at least `width` along a dimension of more than one.
+bool rows_overlap(int64_t tok, int64_t n, int64_t head, int64_t H, int64_t width) {
+  if (n <= 1 || H <= 1) return false;
+  // one dimension steps over the whole of the other (divided, not multiplied: 30 + 38 bits)
+  if (head <= (tok - width) / (H - 1) || tok <= (head - width) / (n - 1)) return false;
+  // t steps of one against h of the other: the two multiples of tok about h * head
+  for (int64_t h = 1; h < H; ++h) {
+    const int64_t t = h * head / tok;
+    if (t > n - 1) break;
+    if (h * head - t * tok < width) return true;
+    if (t + 1 <= n - 1 && (t + 1) * tok - h * head < width) return true;
+  }
+  return false;
+}
+
 size_t write_kv_workspace(const mla_write_kv_args_t* a) {
   const int n_tok = a->B * a->s_q;
   return align_up(256 + (size_t)write_kv_k_split(n_tok, a->d_h) * n_tok * kRow * sizeof(float), 256);
@@ -487,7 +503,7 @@ mla_status_t mla_append_kv(const mla_append_args_t* a, void* stream) {
     if ((st = check_stride(s[0], s[1])) != MLA_OK) return st;
   // outputs whose rows or heads overlap would be written twice
   if ((a->k_pe_out && a->n_tok > 1 && a->k_pe_out_tok < kDr) || (a->H > 0 && a->n_tok > 1 && a->q_pe_out_tok < kDr) ||
-      (a->H > 1 && a->q_pe_out_head < kDr))
+      (a->H > 1 && a->q_pe_out_head < kDr) || rows_overlap(a->q_pe_out_tok, a->n_tok, a->q_pe_out_head, a->H, kDr))
     return MLA_ERR_INVALID_VALUE;
   // in place means the same elements: another stride would read what was written
   if (a->k_pe_out == a->k_pe && a->n_tok > 1 && a->k_pe_out_tok != a->k_pe_tok) return MLA_ERR_INVALID_VALUE;

@@ -476,8 +476,9 @@ mla_status_t mla_append_workspace_size(const mla_append_args_t* args, size_t* by
  * A length below n_b or beyond the block table, or cu_seqlens out of order
  * (MLA_ERR_BAD_SEQ_LEN), or a page id outside the cache (MLA_ERR_BAD_BLOCK_TABLE)
  * is recorded in the workspace's status word and the token is skipped, its
- * outputs included.  But for the two that may be written over themselves, outputs
- * overlap neither an input nor themselves.  Gives no early start to the kernels enqueued after it.
+ * outputs included.  But for the two that may be written over their inputs, outputs
+ * overlap neither an input nor one another; strides that put two heads of q_pe_out,
+ * or two rows of an output, on the same values are refused.  Gives no early start to the kernels enqueued after it.
  */
 mla_status_t mla_append_kv(const mla_append_args_t* args, void* stream);
 

@@ -334,3 +334,32 @@ def test_append_single_rows(cuda_lib):
     cuda_lib.mla_append_kv(a)
     assert cuda_lib.mla_get_status(ws) == 0
     check(x, dict(cache=d["cache"].cpu(), scale=d["scale"].cpu(), k=k_out.cpu(), q=q_out.cpu()))
+
+
+@pytest.mark.parametrize("tok,head,H", [
+    (64, 64 * 12 + 8, 16),       # heads outermost, a gap between them
+    (16 * 64 + 24, 64, 16),      # tokens outermost
+    (128, 192, 2),               # each in the other's gaps
+    (72, 72 * 12, 5),
+])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_query_outputs_in_any_order(cuda_lib, tok, head, H, in_place):
+    """Strides of the rotated queries that leave every head of every token to itself;
+    what lies between is not written."""
+    x = make([2, 1] if H == 2 else [5, 7], [70, 9], H, "bf16", seed=15)
+    n = int(x["cu"][-1])
+    want = run(cuda_lib, x)
+    d = {k: v.cuda() for k, v in x.items() if torch.is_tensor(v)}
+    room = torch.full(((n - 1) * tok + (H - 1) * head + 64,), 7.0, dtype=bf16, device="cuda")
+    q_out = room.as_strided((n, H, 64), (tok, head, 1))
+    free = torch.ones(room.shape, dtype=torch.bool, device="cuda")
+    free.as_strided((n, H, 64), (tok, head, 1)).fill_(False)
+    if in_place:
+        q_out.copy_(d["q"])
+    a = cuda_lib.make_append_args(c=d["joint"][:, :512], k_pe=d["joint"][:, 512:576], q_pe=q_out if in_place else d["q"],
+                                  q_pe_out=q_out, kv_cache=d["cache"], kv_scale=None, block_table=d["table"],
+                                  cu_seqlens=d["cu"], seq_lens=d["lens"])
+    ws = cuda_lib.alloc_workspace(a)
+    cuda_lib.mla_append_kv(a)
+    assert cuda_lib.mla_get_status(ws) == 0
+    assert torch.equal(q_out.cpu(), want["q"]) and bool((room[free] == 7).all())

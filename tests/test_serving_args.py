@@ -335,3 +335,23 @@ def test_speculative_step_verifies_all_its_drafts():
     import inspect
     from head_latent_attention_06_b200.step import SpeculativeStep
     assert "num_draft" not in inspect.signature(SpeculativeStep.verify).parameters
+
+
+@pytest.mark.parametrize("n_tok,H,tok,head", [
+    (8, 16, 64, 64),                        # each token's heads are the next token's, one on
+    (8, 16, 128, 64),
+    (2, 16, 64 * 15, 64),                   # the last head alone
+    (8, 16, 1024, 1000),                    # partly over one another
+    (8, 4, 64, 256),                        # heads outermost, too near
+    (8, 128, 4096, 72),                     # far apart in both indices
+    (1 << 30, 128, 1 << 37, 1 << 37),       # no product of theirs fits 64 bits
+])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_refuses_query_outputs_over_one_another(lib, n_tok, H, tok, head, in_place):
+    """Another token's head on the same values: neither stride shows it alone."""
+    a = append_args(n_tok=n_tok, H=H, q_pe_out_tok=tok, q_pe_out_head=head)
+    if in_place:
+        a.q_pe_tok, a.q_pe_head = tok, head
+    else:
+        a.q_pe_out = 0x10000000
+    assert lib.mla_append_kv(ctypes.byref(a), None) == INVALID
