@@ -75,14 +75,17 @@ MLA_DEVI float dot8(const uint4& a, const uint4& b, float acc) {
 }
 
 // Row t of head h over the keys [lo, hi), by one warp: a lane scores one key of
-// every 32 and owns four values of the output.
+// every 32 and owns four values of the output.  6 us per 32 keys where all warps of
+// the GPU are at it, so that 32 rows of some 300000 keys take longer than the block's
+// other warps may wait: `done` counts the steps for them.
 template <bool PE>
-MLA_DEVI void attend_row(const PackedParams& p, int t, int h, int lo, int hi, int lane) {
+MLA_DEVI void attend_row(const PackedParams& p, int t, int h, int lo, int hi, int lane, int* done) {
   const int g = h / p.share;
   const uint4* qn = reinterpret_cast<const uint4*>(p.q_nope + (int64_t)t * p.qn_tok + (int64_t)h * p.qn_head);
   const uint4* qp = reinterpret_cast<const uint4*>(p.q_pe + (int64_t)t * p.qp_tok + (int64_t)h * p.qp_head);
   float m = -CUDART_INF_F, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
   for (int j0 = lo; j0 < hi; j0 += 32) {
+    if (lane == 0) atomicAdd(done, 1);
     const int j = j0 + lane;
     float s = -CUDART_INF_F;
     if (j < hi) {
@@ -291,9 +294,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(words);
   volatile int* abort_flag = words + 1;
   int* issued = words + 2;  // ring items, queries of tile A, of B
+  int* done_over = words + 5;  // steps of rows that are done over
   Plan* plans = reinterpret_cast<Plan*>(sm + C::kBars + kPlanOff);
   const uint64_t wait_ns = p.wait_ns;
-  auto wait = [&](int b, int parity) { return mbar_wait_converged(bar(b), parity & 1, abort_flag, p.status, wait_ns); };
+  auto wait = [&](int b, int parity) {
+    return mbar_wait_converged(bar(b), parity & 1, abort_flag, p.status, wait_ns, done_over);
+  };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive_local(bar(b));
@@ -317,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    issued[0] = issued[1] = issued[2] = 0;
+    issued[0] = issued[1] = issued[2] = *done_over = 0;
     for (int i = 0; i < B_COUNT; ++i) {
       int count = 1;
       if ((i >= B_P && i < B_P + 4) || (i >= B_READ_O && i < B_READ_O + 2)) count = 4;  // a softmax warp each
@@ -774,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t again = __ballot_sync(0xffffffffu, odd); again; again &= again - 1) {
         const int r = __ffs(again) - 1;
         attend_row<PE>(p, __shfl_sync(0xffffffffu, qi, r), h, __shfl_sync(0xffffffffu, lo, r),
-                       __shfl_sync(0xffffffffu, hi, r), lane);
+                       __shfl_sync(0xffffffffu, hi, r), lane, done_over);
       }
     }
   }

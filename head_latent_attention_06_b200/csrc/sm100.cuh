@@ -154,10 +154,11 @@ MLA_DEVI bool mbar_wait(uint32_t addr, uint32_t parity, volatile int* abort, uin
 }
 
 // Converged-warp form: every lane polls, the loop exits uniformly.  Bounded
-// like mbar_wait.
+// like mbar_wait.  `progress`: a count in shared memory that grows while the block is
+// at work that may take longer than the limit; the limit starts again when it has grown.
 template <bool kCluster = false>
 MLA_DEVI bool mbar_wait_converged(uint32_t addr, uint32_t parity, volatile int* abort, uint32_t* status,
-                                  uint64_t limit_ns) {
+                                  uint64_t limit_ns, volatile int* progress = nullptr) {
   if (__all_sync(0xffffffffu, limit_ns <= 1 ? mbar_test_wait<kCluster>(addr, parity)
                                              : mbar_try_wait<kCluster>(addr, parity)))
     return true;
@@ -169,7 +170,8 @@ MLA_DEVI bool mbar_wait_converged(uint32_t addr, uint32_t parity, volatile int* 
     __syncwarp();
     return false;
   }
-  const uint64_t t0 = globaltimer();
+  uint64_t t0 = globaltimer();
+  int seen = 0;
   for (uint32_t it = 1;; ++it) {
     if (__all_sync(0xffffffffu, mbar_try_wait<kCluster>(addr, parity))) return true;
     if ((it & 255u) == 0 || it == 1) {
@@ -178,9 +180,15 @@ MLA_DEVI bool mbar_wait_converged(uint32_t addr, uint32_t parity, volatile int* 
         if (*abort) {
           stop = 1;
         } else if (globaltimer() - t0 > limit_ns) {
-          *abort = 1;
-          set_status(status, MLA_ERR_DEVICE_TIMEOUT);
-          stop = 1;
+          const int now = progress ? *progress : 0;
+          if (now != seen) {
+            seen = now;
+            t0 = globaltimer();
+          } else {
+            *abort = 1;
+            set_status(status, MLA_ERR_DEVICE_TIMEOUT);
+            stop = 1;
+          }
         }
       }
       if (__shfl_sync(0xffffffffu, stop, 0)) return false;

@@ -525,7 +525,12 @@ mla_status_t mla_prefill_packed_workspace_size(const mla_prefill_packed_args_t* 
  * 128 without the separate RoPE part.  Scores, softmax statistics and outputs
  * are held in fp32, the softmax weights are rounded to bf16 for the product with
  * v, the output once to bf16.  A token that is not seen has no effect, whatever
- * its values (infinities and NaN included).  out must not overlap an input.
+ * its values (infinities and NaN included).  Rows whose weights or sums leave the
+ * common range of fp32 and bf16 - those that see a NaN or an infinity, those that
+ * share a tile of 128 keys with an infinite or NaN v that they do not see, those with a
+ * score 41 or more above all those of the tiles before, or beyond some 2^28 - are done
+ * over one by one from the definition, two orders of magnitude slower than the
+ * others.  out must not overlap an input.
  * cu_seqlens out of order (MLA_ERR_BAD_SEQ_LEN) goes to the workspace's status
  * word; what the rows of such a batch then hold is not defined.
  */
@@ -604,6 +609,8 @@ mla_status_t mla_set_decode_kernel(int32_t kernel);
  * (process-wide; 0 restores the default of 2 s).  A wait that runs out records
  * MLA_ERR_DEVICE_TIMEOUT in the status word, and the kernel waits for its copies
  * in flight, frees its tensor memory and returns, leaving the context usable.
+ * In mla_prefill_packed a wait goes on while rows are done over (see there): that
+ * work ends by itself, but may take longer than the limit.
  * Takes effect for launches after it returns (a CUDA graph keeps the limit it
  * captured).  A limit of 1 ns gives up at the first wait that a non-blocking
  * test finds unsatisfied (the device clock may advance in steps much coarser

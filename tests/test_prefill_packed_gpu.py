@@ -444,3 +444,21 @@ def test_packed_scores_beyond_the_exponent_range(cuda_lib, small, causal):
     o, lse, mass, _ = oracle_of(x, causal)
     assert (np.abs(to_np(x["out"]) - o) <= 2.0 ** -8 * np.abs(o) + (2.0 ** -8 + 2.0 ** -20) * mass).all()
     assert (np.abs(to_np(x["lse"]) - lse) <= 2.0 ** -21 * np.abs(lse)).all()
+
+
+def test_packed_rows_done_over_outlast_the_wait_limit(cuda_lib):
+    """A prompt whose every row sees a NaN is done over by single warps, 32 rows of up to
+    16000 keys each, far longer than the limit set here, while the block's other warps
+    wait: that is progress, not a wait that ran out.  The prompt beside it comes out
+    right."""
+    lens = [200, 16000]
+    x = make(lens, 10, 10, 64, seed=21)
+    ref_rows = [0, 57, 199]
+    x["k_nope"][200] = float("nan")
+    cuda_lib.mla_set_device_wait_limit(5_000_000)
+    try:
+        assert run(cuda_lib, x) == 0
+    finally:
+        cuda_lib.mla_set_device_wait_limit(0)
+    check_rows(x, ref_rows)
+    assert bool(torch.isnan(x["out"][200:]).all())
