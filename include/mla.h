@@ -583,8 +583,8 @@ mla_status_t mla_verify_workspace_size(const mla_verify_args_t* args, size_t* by
  *   next token = the smallest j with w_0 + .. + w_j > u_sample (w_0 + .. + w_(V-1))
  * num_accepted = a, tokens = x_0 .. x_(a-1), next, -1 .., new_lens = seq_lens - (n - a).
  * Differences are exact, the sums carry the rounding errors of 32-bit steps along
- * and are joined in fp64: u within some 1e-12 of a boundary, relative to the sum,
- * may fall on either side, the same side every time.  Probabilities below zero
+ * and are joined in fp64: u within 2^-36 (1.5e-11) of a boundary, relative to the
+ * sum, may fall on either side, the same side every time.  Probabilities below zero
  * count as zero in w, and so does a weight that is NaN; the next token is -1 when
  * nothing is left, a p_a(j) is infinite or the sum is beyond fp32.  A draft outside [0, V) (MLA_ERR_BAD_TOKEN)
  * or num_draft outside [0, s_q - 1] (MLA_ERR_BAD_SEQ_LEN) is recorded in the
