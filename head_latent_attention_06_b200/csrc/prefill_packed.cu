@@ -27,8 +27,9 @@
 // Measured (us; in long runs back to back, and over a few tens of passes): one prompt of
 // 4096 tokens, 128 heads 630 and 555 (1.09 and 1.24 PFLOP/s; cuBLAS 1.38 and 1.62); 7
 // prompts of 5120 tokens, 128 heads 391 and 354; 5 prompts of 7001 tokens, 32 heads in
-// groups of 4 without the RoPE part 141 and 125; 67 prompts of 8191 tokens, 16 heads 57
-// and 55; one of 17 tokens 6.8.
+// groups of 4 without the RoPE part 141 and 127; 67 prompts of 8191 tokens, 16 heads 57
+// and 56; one of 17 tokens 6.8 to 7.5.  The causal form of one prompt of 4096 tokens, 32
+// heads 160, not causal 268 (twice the products).
 #include <math_constants.h>
 
 #include "packed.cuh"
@@ -659,8 +660,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The weights are 2^(s scale - m) for a reference m near the row's maximum so far,
         // not the maximum itself: any m gives the same quotient, as long as the weights
         // and their sums stay within fp32 and bf16's common range.  So m is found where
-        // there is none and raised one tile after a weight went beyond 2^8; the hot loop
-        // takes no maximum.
+        // there is none and raised one tile after a weight went beyond 2^8; the loop over
+        // rows that all have a reference takes no maximum.  A warp in which some row has
+        // none yet (its sequence begins later, or it is of no sequence) takes one every
+        // tile: one prompt of 4097 tokens, 128 heads 660 us, of 4224 tokens, where no warp
+        // has such rows, 640.
         if (__any_sync(0xffffffffu, stale)) {
           float m4[4];
 #pragma unroll
