@@ -25,8 +25,8 @@
 // softmax, 1024 of them exponentials at the special-function units' rate.
 //
 // Measured (us; in long runs back to back, and over a few tens of passes): one prompt of
-// 4096 tokens, 128 heads 630 and 555 (1.09 and 1.24 PFLOP/s; cuBLAS 1.38 and 1.62); 7
-// prompts of 5120 tokens, 128 heads 391 and 354; 5 prompts of 7001 tokens, 32 heads in
+// 4096 tokens, 128 heads 637 and 550 (1.08 and 1.25 PFLOP/s; cuBLAS 1.38 and 1.62); 7
+// prompts of 5120 tokens, 128 heads 392 and 337 to 354; 5 prompts of 7001 tokens, 32 heads in
 // groups of 4 without the RoPE part 141 and 127; 67 prompts of 8191 tokens, 16 heads 57
 // and 56; one of 17 tokens 6.8 to 7.5.  The causal form of one prompt of 4096 tokens, 32
 // heads 160, not causal 268 (twice the products).
